@@ -20,3 +20,10 @@ from .binding import (  # noqa: F401
     moe_unpermute,
     moe_unpermute_local,
 )
+from .experts import (  # noqa: F401
+    moe_grouped_gated_gemm_backward_bf16,
+    moe_grouped_gated_gemm_bf16,
+    moe_grouped_linear_backward_bf16,
+    moe_grouped_linear_bf16,
+    moe_unpermute_backward,
+)
