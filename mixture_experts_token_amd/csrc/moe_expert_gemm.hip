@@ -1,4 +1,4 @@
-// moe_expert_gemm.hip -- the expert layers' grouped products (gfx950).
+// moe_expert_gemm.hip -- the expert layers' grouped products (gfx950 MFMA).
 //
 // One product per expert e, over the rows the permute made contiguous (vLLM
 // PR #14568, PR description), with the operands laid out as the layer keeps
@@ -7,8 +7,12 @@
 //   input grad    d_x[j][i] = sum_T d_z[j][T] w[e][T][i]
 //   weight grad   d_w[e][c][i] = sum_T d_z[off[e] + T][c] x[off[e] + T][i]
 //
-// 64 x 64 tiles of fp32 sums in registers, operands widened to fp32 in LDS, 16
-// of T at a time.
+// Tiles of 256 x 256 outputs (moe_expert_tile.h), bf16 operands, fp32 sums.
+// The tile list is derived on the device from the offsets; every workgroup
+// (one per CU) walks it persistently.  A gated forward tile holds 128 gate
+// columns and the 128 up columns that belong to them, arranged so that a
+// wave's two 32-column blocks are a gate block and its up block: the product
+// of the two is then within a lane.
 
 #include <hip/hip_runtime.h>
 
@@ -16,6 +20,7 @@
 
 #include "moe_expert_device.h"
 #include "moe_expert_launch.h"
+#include "moe_expert_tile.h"
 
 namespace moe {
 
@@ -23,7 +28,8 @@ namespace {
 
 enum class Product { kForward, kInputGrad, kWeightGrad };
 
-constexpr int kTile = 64, kDepth = 16, kGemmThreads = 256;
+constexpr int kXcdCount = 8;
+constexpr int64_t kGroupRows = 8;  // row tiles per group in the tile order
 
 struct GemmParams {
     const int64_t* off;
@@ -39,98 +45,148 @@ struct GemmParams {
     uint16_t* out;
 };
 
+// Four consecutive outputs as bf16 (8 bytes).
+__device__ __forceinline__ void store4(uint16_t* dst, float v0, float v1, float v2, float v3) {
+    *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16(v0, v1), pack_bf16(v2, v3)};
+}
+
 template <Product kP, bool kGated, int kAct>
-__global__ __launch_bounds__(kGemmThreads) void expert_product_kernel(GemmParams p) {
-    __shared__ float as[kDepth][kTile + 1];
-    __shared__ float bs[kGated ? 2 : 1][kDepth][kTile + 1];
+__global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmParams p) {
+    constexpr bool kATc = kP != Product::kWeightGrad;  // x, d_z rows: T-contiguous
+    constexpr bool kBTc = kP == Product::kForward;     // w rows
+    constexpr int kColsPerTile = kGated ? kTileCols / 2 : kTileCols;
+    __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
     __shared__ int64_t pre_s[kMaxExperts + 1];
-    __shared__ int64_t part[kGemmThreads / 64];
+    __shared__ int64_t part[kTileThreads / 64];
     const int64_t cols = kP == Product::kForward ? p.n : p.k;
-    const int64_t col_tiles = (cols + kTile - 1) / kTile;
-    const bool ok = expert_items<kGemmThreads>(p.off, p.num_experts, p.max_rows, pre_s, part, [&](int64_t rows) {
+    const int64_t col_tiles = (cols + kColsPerTile - 1) / kColsPerTile;
+    const bool ok = expert_items<kTileThreads>(p.off, p.num_experts, p.max_rows, pre_s, part, [&](int64_t rows) {
         const int64_t r = kP == Product::kWeightGrad ? p.m : rows;
-        return (r + kTile - 1) / kTile * col_tiles;
+        return (r + kTileRows - 1) / kTileRows * col_tiles;
     });
     if (!ok) return;
-    const int64_t total = pre_s[p.num_experts];
-    const int tid = threadIdx.x, tr = tid / 16 * 4, tc = tid % 16 * 4;
-    for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
+    const int64_t total = wave_uniform64(pre_s[p.num_experts]);
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wm = wave / 4, wn = wave % 4;
+    // Workgroups are dispatched round-robin over the XCDs; the tiles running at
+    // once are split into one contiguous chunk per XCD, so that an XCD's L2
+    // serves neighbouring tiles.
+    const int64_t grid = gridDim.x;
+    const int64_t slot = (int64_t)(blockIdx.x % kXcdCount) * (grid / kXcdCount) + blockIdx.x / kXcdCount;
+    for (int64_t id = slot; id < total; id += grid) {
         const int e = expert_of_item(pre_s, p.num_experts, id);
-        const int64_t r0 = (id - pre_s[e]) / col_tiles * kTile, c0 = (id - pre_s[e]) % col_tiles * kTile;
-        const int64_t first = p.off[e], count = p.off[e + 1] - first;
+        const int64_t first = wave_uniform64(p.off[e]), count = wave_uniform64(p.off[e + 1]) - first;
         const int64_t rows = kP == Product::kWeightGrad ? p.m : count;
-        const int64_t depth = kP == Product::kForward ? p.k : kP == Product::kInputGrad ? p.m : count;
-        float acc[kGated ? 2 : 1][4][4] = {};
-        for (int64_t t0 = 0; t0 < depth; t0 += kDepth) {
-            __syncthreads();
-            for (int i = tid; i < kTile * kDepth; i += kGemmThreads) {
-                // consecutive threads along the operand's contiguous direction
-                const bool a_t_major = kP == Product::kWeightGrad, b_t_major = kP != Product::kForward;
-                const int at = a_t_major ? i / kTile : i % kDepth, ar = a_t_major ? i % kTile : i / kDepth;
-                const int bt = b_t_major ? i / kTile : i % kDepth, bc = b_t_major ? i % kTile : i / kDepth;
-                float av = 0.0f;
-                if (t0 + at < depth && r0 + ar < rows) {
-                    if (kP == Product::kForward) av = bf16_to_float(p.a[(first + r0 + ar) * p.k + t0 + at]);
-                    if (kP == Product::kInputGrad) av = bf16_to_float(p.a[(first + r0 + ar) * p.m + t0 + at]);
-                    if (kP == Product::kWeightGrad) av = bf16_to_float(p.a[(first + t0 + at) * p.m + r0 + ar]);
-                }
-                as[at][ar] = av;
-#pragma unroll
-                for (int g = 0; g < (kGated ? 2 : 1); ++g) {
-                    float bv = 0.0f;
-                    if (t0 + bt < depth && c0 + bc < cols) {
-                        if (kP == Product::kForward)
-                            bv = bf16_to_float(p.b[((int64_t)e * p.m + g * p.n + c0 + bc) * p.k + t0 + bt]);
-                        if (kP == Product::kInputGrad)
-                            bv = bf16_to_float(p.b[((int64_t)e * p.m + t0 + bt) * p.k + c0 + bc]);
-                        if (kP == Product::kWeightGrad) bv = bf16_to_float(p.b[(first + t0 + bt) * p.k + c0 + bc]);
-                    }
-                    bs[g][bt][bc] = bv;
-                }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int t = 0; t < kDepth; ++t)
-#pragma unroll
-                for (int g = 0; g < (kGated ? 2 : 1); ++g)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[g][i][j] = __builtin_fmaf(as[t][tr + i], bs[g][t][tc + j], acc[g][i][j]);
+        // Groups of kGroupRows row tiles, within a group row tiles fastest; a
+        // remainder of up to three joins the last group (it would stream every
+        // column tile again for itself).
+        const int64_t local = id - wave_uniform64(pre_s[e]);
+        const int64_t mt = (rows + kTileRows - 1) / kTileRows;
+        const int64_t groups = mt % kGroupRows <= 3 && mt >= kGroupRows ? mt / kGroupRows : (mt + kGroupRows - 1) / kGroupRows;
+        const int64_t g0 = local / (kGroupRows * col_tiles), g = g0 < groups - 1 ? g0 : groups - 1;
+        const int64_t gsize = g == groups - 1 ? mt - g * kGroupRows : kGroupRows;
+        const int64_t in_group = local - g * kGroupRows * col_tiles;
+        const int64_t r0 = wave_uniform64((g * kGroupRows + in_group % gsize) * kTileRows);
+        const int64_t c0 = wave_uniform64(in_group / gsize * kColsPerTile);
+        const int64_t rows_left = rows - r0 < kTileRows ? rows - r0 : kTileRows;
+        const int64_t cols_left = cols - c0 < kColsPerTile ? cols - c0 : kColsPerTile;
+
+        OperandView a{}, b{};
+        int a_row = wave * 16, b_row = wave * 16;
+        uint32_t a_half, b_half;
+        if constexpr (kP == Product::kForward) {
+            a.first = reinterpret_cast<const char*>(p.a + (first + r0) * p.k);
+            a.rows_bytes = b.rows_bytes = p.k * 2;
+            a.depth = b.depth = p.k;
+            a.extent = rows_left;
+            b.extent = cols_left;
+            const bool up = kGated && wave % 4 >= 2;  // which rows of w this wave loads
+            if constexpr (kGated) b_row = wave / 4 * 32 + wave % 2 * 16;
+            b.first = reinterpret_cast<const char*>(p.b + ((int64_t)e * p.m + (up ? p.n : 0) + c0) * p.k);
+            a_half = (uint32_t)(128 * a.rows_bytes);
+            b_half = (uint32_t)((kGated ? 64 : 128) * b.rows_bytes);
+        } else if constexpr (kP == Product::kInputGrad) {
+            a.first = reinterpret_cast<const char*>(p.a + (first + r0) * p.m);
+            a.rows_bytes = p.m * 2;
+            a.depth = b.depth = p.m;
+            a.extent = rows_left;
+            b.first = reinterpret_cast<const char*>(p.b + (int64_t)e * p.m * p.k + c0);
+            b.rows_bytes = p.k * 2;
+            b.col_bytes = c0 * 2;
+            b_row = wave * 8;
+            a_half = (uint32_t)(128 * a.rows_bytes);
+            b_half = 256;
+        } else {
+            a.first = reinterpret_cast<const char*>(p.a + first * p.m + r0);
+            b.first = reinterpret_cast<const char*>(p.b + first * p.k + c0);
+            a.rows_bytes = p.m * 2;
+            b.rows_bytes = p.k * 2;
+            a.col_bytes = r0 * 2;
+            b.col_bytes = c0 * 2;
+            a.depth = b.depth = count;
+            a_row = b_row = wave * 8;
+            a_half = b_half = 256;
         }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int64_t r = r0 + tr + i, c = c0 + tc + j;
-                if (r >= rows || c >= cols) continue;
-                if constexpr (kP == Product::kForward) {
-                    const int64_t row = first + r;
-                    float z = acc[0][i][j];
-                    if constexpr (kGated) {
-                        const float u = acc[1][i][j];
-                        if (p.pre != nullptr) {
-                            p.pre[row * p.m + c] = (uint16_t)float_to_bf16(z);
-                            p.pre[row * p.m + p.n + c] = (uint16_t)float_to_bf16(u);
+        TileSums sums;
+        tile_sums<kATc, kBTc>(lds, a, b, a_row, b_row, a_half, b_half, sums);
+
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const int64_t r = h * 128 + wm * 64 + f * 32 + lane % 32;
+                if (r >= rows_left) continue;
+                const int64_t row = (kP == Product::kWeightGrad ? (int64_t)e * p.m : first) + r0 + r;
+#pragma unroll
+                for (int cb = 0; cb < (kGated ? 1 : 2); ++cb)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int64_t cl = (kGated ? wn * 32 : wn * 64 + cb * 32) + j * 8 + lane / 32 * 4;
+                        if (cl >= cols_left) continue;
+                        const int64_t c = c0 + cl;
+                        float z[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) z[q] = sums.v[h][f][cb][4 * j + q];
+                        if constexpr (kGated) {
+                            float u[4], y[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                u[q] = sums.v[h][f][1][4 * j + q];
+                                y[q] = act_value<kAct>(z[q]) * u[q];
+                            }
+                            if (p.pre != nullptr) {
+                                store4(p.pre + row * p.m + c, z[0], z[1], z[2], z[3]);
+                                store4(p.pre + row * p.m + p.n + c, u[0], u[1], u[2], u[3]);
+                            }
+                            store4(p.out + row * p.n + c, y[0], y[1], y[2], y[3]);
+                        } else if constexpr (kP == Product::kForward) {
+                            if (p.bias != nullptr) {
+                                const u32x2 bv = *reinterpret_cast<const u32x2*>(p.bias + (int64_t)e * p.n + c);
+                                z[0] += bf16_low(bv[0]), z[1] += bf16_high(bv[0]);
+                                z[2] += bf16_low(bv[1]), z[3] += bf16_high(bv[1]);
+                            }
+                            if (p.pre != nullptr) store4(p.pre + row * p.n + c, z[0], z[1], z[2], z[3]);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) z[q] = act_value<kAct>(z[q]);
+                            if (p.residual != nullptr) {
+                                const u32x2 rv = *reinterpret_cast<const u32x2*>(p.residual + row * p.n + c);
+                                z[0] += bf16_low(rv[0]), z[1] += bf16_high(rv[0]);
+                                z[2] += bf16_low(rv[1]), z[3] += bf16_high(rv[1]);
+                            }
+                            store4(p.out + row * p.n + c, z[0], z[1], z[2], z[3]);
+                        } else {
+                            store4(p.out + row * p.k + c, z[0], z[1], z[2], z[3]);
                         }
-                        p.out[row * p.n + c] = (uint16_t)float_to_bf16(act_value<kAct>(z) * u);
-                    } else {
-                        if (p.bias != nullptr) z += bf16_to_float(p.bias[(int64_t)e * p.n + c]);
-                        if (p.pre != nullptr) p.pre[row * p.n + c] = (uint16_t)float_to_bf16(z);
-                        float y = act_value<kAct>(z);
-                        if (p.residual != nullptr) y += bf16_to_float(p.residual[row * p.n + c]);
-                        p.out[row * p.n + c] = (uint16_t)float_to_bf16(y);
                     }
-                } else {
-                    const int64_t row = kP == Product::kInputGrad ? first + r : (int64_t)e * p.m + r;
-                    p.out[row * p.k + c] = (uint16_t)float_to_bf16(acc[0][i][j]);
-                }
             }
     }
 }
 
 template <Product kP, bool kGated, int kAct>
 hipError_t launch_product(const GemmParams& p, int num_cus, hipStream_t stream) {
-    hipLaunchKernelGGL((expert_product_kernel<kP, kGated, kAct>), dim3((unsigned)num_cus * 8), dim3(kGemmThreads), 0,
+    const int blocks = num_cus < kXcdCount ? kXcdCount : num_cus / kXcdCount * kXcdCount;
+    hipLaunchKernelGGL((expert_product_kernel<kP, kGated, kAct>), dim3((unsigned)blocks), dim3(kTileThreads), 0,
                        stream, p);
     return hipGetLastError();
 }
