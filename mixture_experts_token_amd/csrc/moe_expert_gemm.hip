@@ -45,9 +45,21 @@ struct GemmParams {
     uint16_t* out;
 };
 
-// Four consecutive outputs as bf16 (8 bytes).
-__device__ __forceinline__ void store4(uint16_t* dst, float v0, float v1, float v2, float v3) {
-    *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16(v0, v1), pack_bf16(v2, v3)};
+// Calls f(row of the tile, column of the wave's 32-column block cb, values) for
+// every run of four consecutive outputs this lane holds of block cb.
+template <typename F>
+__device__ __forceinline__ void for_each_run(const TileSums& sums, int cb, int wm, int lane, F&& f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int fb = 0; fb < 2; ++fb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = sums.v[h][fb][cb][4 * j + q];
+                f(h * 128 + wm * 64 + fb * 32 + lane % 32, j * 8 + lane / 32 * 4, v);
+            }
 }
 
 template <Product kP, bool kGated, int kAct>
@@ -66,7 +78,6 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
     });
     if (!ok) return;
     const int64_t total = wave_uniform64(pre_s[p.num_experts]);
-    const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int wm = wave / 4, wn = wave % 4;
     // Workgroups are dispatched round-robin over the XCDs; the tiles running at
@@ -131,55 +142,95 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
         TileSums sums;
         tile_sums<kATc, kBTc>(lds, a, b, a_row, b_row, a_half, b_half, sums);
 
+        const int lane = opaque_lane();
+        const int64_t row0 = (kP == Product::kWeightGrad ? (int64_t)e * p.m : first) + r0;
+        const int rl = (int)rows_left, cl = (int)cols_left;
+        if constexpr (kGated) {
+            using Out = StagedTile<kTileCols / 2>;
+            // gate and up go out first, as they are; h after them
+            if (p.pre != nullptr) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const int64_t r = h * 128 + wm * 64 + f * 32 + lane % 32;
-                if (r >= rows_left) continue;
-                const int64_t row = (kP == Product::kWeightGrad ? (int64_t)e * p.m : first) + r0 + r;
-#pragma unroll
-                for (int cb = 0; cb < (kGated ? 1 : 2); ++cb)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int64_t cl = (kGated ? wn * 32 : wn * 64 + cb * 32) + j * 8 + lane / 32 * 4;
-                        if (cl >= cols_left) continue;
-                        const int64_t c = c0 + cl;
-                        float z[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) z[q] = sums.v[h][f][cb][4 * j + q];
-                        if constexpr (kGated) {
-                            float u[4], y[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                u[q] = sums.v[h][f][1][4 * j + q];
-                                y[q] = act_value<kAct>(z[q]) * u[q];
-                            }
-                            if (p.pre != nullptr) {
-                                store4(p.pre + row * p.m + c, z[0], z[1], z[2], z[3]);
-                                store4(p.pre + row * p.m + p.n + c, u[0], u[1], u[2], u[3]);
-                            }
-                            store4(p.out + row * p.n + c, y[0], y[1], y[2], y[3]);
-                        } else if constexpr (kP == Product::kForward) {
-                            if (p.bias != nullptr) {
-                                const u32x2 bv = *reinterpret_cast<const u32x2*>(p.bias + (int64_t)e * p.n + c);
-                                z[0] += bf16_low(bv[0]), z[1] += bf16_high(bv[0]);
-                                z[2] += bf16_low(bv[1]), z[3] += bf16_high(bv[1]);
-                            }
-                            if (p.pre != nullptr) store4(p.pre + row * p.n + c, z[0], z[1], z[2], z[3]);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) z[q] = act_value<kAct>(z[q]);
-                            if (p.residual != nullptr) {
-                                const u32x2 rv = *reinterpret_cast<const u32x2*>(p.residual + row * p.n + c);
-                                z[0] += bf16_low(rv[0]), z[1] += bf16_high(rv[0]);
-                                z[2] += bf16_low(rv[1]), z[3] += bf16_high(rv[1]);
-                            }
-                            store4(p.out + row * p.n + c, z[0], z[1], z[2], z[3]);
-                        } else {
-                            store4(p.out + row * p.k + c, z[0], z[1], z[2], z[3]);
-                        }
-                    }
+                for (int g = 0; g < 2; ++g) {
+                    char* half = lds + g * (kTileLds / 2);
+                    for_each_run(sums, g, wm, lane,
+                                 [&](int r, int c, const float(&v)[4]) { Out::put(half, r, wn * 32 + c, v); });
+                }
+                lds_phase_barrier();
+                Out::store(lds, p.pre + row0 * p.m + c0, p.m, rl, cl, wave, lane);
+                Out::store(lds + kTileLds / 2, p.pre + row0 * p.m + p.n + c0, p.m, rl, cl, wave, lane);
+                lds_phase_barrier();
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sums.v[h][f][0][i] = act_value<kAct>(sums.v[h][f][0][i]) * sums.v[h][f][1][i];
+            for_each_run(sums, 0, wm, lane,
+                         [&](int r, int c, const float(&v)[4]) { Out::put(lds, r, wn * 32 + c, v); });
+            lds_phase_barrier();
+            Out::store(lds, p.out + row0 * p.n + c0, p.n, rl, cl, wave, lane);
+        } else {
+            using Out = StagedTile<kTileCols>;
+            uint16_t* out = p.out + row0 * cols + c0;
+            if constexpr (kP == Product::kForward) {
+                if (p.bias != nullptr) {
+#pragma unroll
+                    for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int c = wn * 64 + cb * 32 + j * 8 + lane / 32 * 4;
+                            u32x2 bv = {0u, 0u};
+                            if (c < cl) bv = *reinterpret_cast<const u32x2*>(p.bias + (int64_t)e * p.n + c0 + c);
+                            const float bias[4] = {bf16_low(bv[0]), bf16_high(bv[0]), bf16_low(bv[1]), bf16_high(bv[1])};
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) sums.v[h][f][cb][4 * j + q] += bias[q];
+                        }
+                }
+                if (p.pre != nullptr) {
+#pragma unroll
+                    for (int cb = 0; cb < 2; ++cb)
+                        for_each_run(sums, cb, wm, lane, [&](int r, int c, const float(&v)[4]) {
+                            Out::put(lds, r, wn * 64 + cb * 32 + c, v);
+                        });
+                    lds_phase_barrier();
+                    Out::store(lds, p.pre + row0 * p.n + c0, p.n, rl, cl, wave, lane);
+                    lds_phase_barrier();
+                }
+                if (p.residual != nullptr) {
+                    // the residual's tile, where the result will stand
+                    Out::load(lds, p.residual + row0 * p.n + c0, p.n, rl, wave, lane, c0 * 2);
+                    wait_loads<0>();
+                    lds_phase_barrier();
+                }
+            }
+#pragma unroll
+            for (int cb = 0; cb < 2; ++cb)
+                for_each_run(sums, cb, wm, lane, [&](int r, int c, const float(&v)[4]) {
+                    const int col = wn * 64 + cb * 32 + c;
+                    if constexpr (kP == Product::kForward) {
+                        float y[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) y[q] = act_value<kAct>(v[q]);
+                        if (p.residual != nullptr) {
+                            const u32x2 rv = *Out::at(lds, r, col);
+                            y[0] += bf16_low(rv[0]), y[1] += bf16_high(rv[0]);
+                            y[2] += bf16_low(rv[1]), y[3] += bf16_high(rv[1]);
+                        }
+                        Out::put(lds, r, col, y);
+                    } else {
+                        Out::put(lds, r, col, v);
+                    }
+                });
+            lds_phase_barrier();
+            Out::store(lds, out, cols, rl, cl, wave, lane);
+        }
+        lds_phase_barrier();  // the stages are free for the next tile
     }
 }
 

@@ -49,6 +49,15 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
+// The lane index as a value the compiler cannot see through: what is derived
+// from it in a tile's epilogue is computed there, not kept in registers through
+// the k-loop.
+__device__ __forceinline__ int opaque_lane() {
+    int lane = (int)(threadIdx.x % 64);
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // Barrier of the pipeline.  Nothing moves across it, MFMAs included (they
 // touch no memory, so a fence alone would not hold them); loads in flight are
 // not waited for.
@@ -236,8 +245,8 @@ __device__ __forceinline__ void multiply(const Frags& a, const Frags& b, f32x16 
 template <bool kATc, bool kBTc>
 __device__ __forceinline__ void tile_sums(char* lds, const OperandView& a, const OperandView& b, int a_row, int b_row,
                                           uint32_t a_half, uint32_t b_half, TileSums& sums) {
-    const int tid = threadIdx.x, lane = tid % 64;
-    const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int lane = opaque_lane();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int wm = wave / 4, wn = wave % 4;
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
     const uint32_t a_voff[2] = {load_offset<kATc>(a.rows_bytes, a_row, lane, 0),
@@ -298,5 +307,67 @@ __device__ __forceinline__ void tile_sums(char* lds, const OperandView& a, const
     wait_loads<0>();
     phase_barrier();
 }
+
+// Barrier around the epilogue's use of LDS: this wave's LDS accesses are done
+// before it arrives; stores in flight are not waited for.
+__device__ __forceinline__ void lds_phase_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A finished tile in LDS: 256 rows of kCols bf16, the 16-byte units of a row
+// XOR-swizzled by the row so that the 16 rows of an 8-byte write's phase touch
+// different banks.  Results go out through it as whole rows: stored straight
+// from the MFMA layout, an instruction writes 16 bytes of each of 32 rows, and
+// those partial lines cost more than the product of a short T (see below).
+template <int kCols>
+struct StagedTile {
+    static constexpr int kUnits = kCols / 8, kPitch = kCols * 2;
+    static constexpr int kRowsPerLoad = 1024 / kPitch, kInstr = kTileRows / 8 / kRowsPerLoad;
+    static_assert(kTileRows * kPitch <= kTileLds, "a staged tile fits the stages");
+
+    // Address of columns col .. col + 3 (col a multiple of 4) of a row.
+    static __device__ __forceinline__ u32x2* at(char* lds, int row, int col) {
+        return reinterpret_cast<u32x2*>(lds + row * kPitch + ((col / 8) ^ (row % kUnits)) * 16 + col % 8 * 2);
+    }
+    static __device__ __forceinline__ void put(char* lds, int row, int col, const float (&v)[4]) {
+        *at(lds, row, col) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    }
+    // Row and 16-byte unit of this lane in instruction i of its wave.
+    static __device__ __forceinline__ int lane_row(int wave, int lane, int i) {
+        return wave * (kTileRows / 8) + i * kRowsPerLoad + lane / kUnits;
+    }
+    // The whole tile (after a barrier) to dst, rows `stride` elements apart.
+    static __device__ __forceinline__ void store(const char* lds, uint16_t* dst, int64_t stride, int rows, int cols,
+                                                 int wave, int lane) {
+        u32x4 v[kInstr];
+        const int unit = lane % kUnits;
+#pragma unroll
+        for (int i = 0; i < kInstr; ++i) {
+            const int r = lane_row(wave, lane, i);
+            v[i] = *reinterpret_cast<const u32x4*>(lds + r * kPitch + (unit ^ (r % kUnits)) * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < kInstr; ++i) {
+            const int r = lane_row(wave, lane, i);
+            if (r < rows && unit * 8 < cols) *reinterpret_cast<u32x4*>(dst + r * stride + unit * 8) = v[i];
+        }
+    }
+    // The whole tile from src straight into LDS; waited for by the caller.
+    static __device__ __forceinline__ void load(char* lds, const uint16_t* src, int64_t stride, int rows, int wave,
+                                                int lane, int64_t col_bytes) {
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)wave_uniform64((int64_t)src), 0,
+            __builtin_amdgcn_readfirstlane((int)(rows * stride * 2 - col_bytes)), 0x00020000);
+#pragma unroll
+        for (int i = 0; i < kInstr; ++i) {
+            const int r = lane_row(wave, lane, i);
+            const int off = (int)(r * stride * 2) + ((lane % kUnits) ^ (r % kUnits)) * 16;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * kInstr + i) * 1024), 16, off, 0, 0, 0);
+        }
+    }
+};
 
 }  // namespace moe
