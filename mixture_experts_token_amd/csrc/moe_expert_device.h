@@ -21,14 +21,13 @@ __device__ __forceinline__ float bf16_to_float(uint32_t bits) { return __uint_as
 __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// fp32 -> bf16, to nearest, ties to even; NaN stays a (quiet) NaN.
-__device__ __forceinline__ uint32_t float_to_bf16(float f) {
-    const uint32_t u = __float_as_uint(f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
+// Two fp32 -> two bf16 (lo in the low half), to nearest, ties to even; NaN stays
+// a quiet NaN.  One v_cvt_pk_bf16_f32; the same rounding in integer
+// instructions took a third of a short product's epilogue.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    return float_to_bf16(lo) | (float_to_bf16(hi) << 16);
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 // A value every lane of the wave holds, moved into a scalar register.

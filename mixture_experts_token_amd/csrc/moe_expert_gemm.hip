@@ -45,35 +45,85 @@ struct GemmParams {
     uint16_t* out;
 };
 
-// Calls f(row of the tile, column of the wave's 32-column block cb, values) for
-// every run of four consecutive outputs this lane holds of block cb.
+// Quotient and remainder of non-negative scalars; 32 bits when both fit (a
+// 64-bit division is a long sequence of instructions).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t& rem) {
+    int64_t q;
+    if (((a | b) >> 32) == 0) q = (int64_t)((uint32_t)a / (uint32_t)b);
+    else q = a / b;
+    rem = a - q * b;
+    return q;
+}
+
+struct TileCoord {
+    int expert;
+    int64_t first, count;  // the expert's rows
+    int64_t r0, c0;        // the tile's first output row (of the expert's) and column
+};
+
+// Order of an expert's tiles: groups of kGroupRows row tiles, within a group
+// row tiles fastest, then column tiles; a remainder of up to three row tiles
+// joins the last group (it would stream every column tile again for itself).
+template <bool kWeightGrad>
+__device__ __forceinline__ TileCoord tile_coord(int64_t id, const int64_t* pre, const int64_t* off, int num_experts,
+                                                int64_t m, int64_t col_tiles, int cols_per_tile) {
+    TileCoord t;
+    t.expert = expert_of_item(pre, num_experts, id);
+    t.first = wave_uniform64(off[t.expert]);
+    t.count = wave_uniform64(off[t.expert + 1]) - t.first;
+    const int64_t local = id - wave_uniform64(pre[t.expert]);
+    const int64_t mt = ((kWeightGrad ? m : t.count) + kTileRows - 1) / kTileRows;
+    const int64_t left = mt % kGroupRows;
+    const int64_t groups = mt / kGroupRows + (left > 3 || mt < kGroupRows);
+    int64_t rem;
+    const int64_t g0 = divide(local, kGroupRows * col_tiles, rem), g = g0 < groups - 1 ? g0 : groups - 1;
+    const int64_t gsize = g == groups - 1 ? mt - g * kGroupRows : kGroupRows;
+    const int64_t ct = divide(local - g * kGroupRows * col_tiles, gsize, rem);
+    t.r0 = wave_uniform64((g * kGroupRows + rem) * kTileRows);
+    t.c0 = wave_uniform64(ct * cols_per_tile);
+    return t;
+}
+
+// Calls f(row of the tile, column within the wave's 32-column block, values
+// even, values odd) for every pair of runs (columns 16 p + 4 (l / 32) .. and 8
+// further) of row block (h, fb): the column given is that of the pair's vector.
 template <typename F>
-__device__ __forceinline__ void for_each_run(const TileSums& sums, int cb, int wm, int lane, F&& f) {
+__device__ __forceinline__ void for_each_pair(int wm, int lane, F&& f) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int fb = 0; fb < 2; ++fb)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float v[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = sums.v[h][fb][cb][4 * j + q];
-                f(h * 128 + wm * 64 + fb * 32 + lane % 32, j * 8 + lane / 32 * 4, v);
-            }
+            for (int p = 0; p < 2; ++p) f(h, fb, p, h * 128 + wm * 64 + fb * 32 + lane % 32, p * 16 + lane / 32 * 8);
+}
+
+__device__ __forceinline__ u32x2 pack4(const f32x16& v, int j) {
+    return u32x2{pack_bf16(v[4 * j], v[4 * j + 1]), pack_bf16(v[4 * j + 2], v[4 * j + 3])};
+}
+__device__ __forceinline__ u32x4 pack_pair(const f32x16& v, int p) {
+    return runs_to_vector(pack4(v, 2 * p), pack4(v, 2 * p + 1));
+}
+__device__ __forceinline__ void add4(f32x16& v, int j, u32x2 w) {
+    v[4 * j] += bf16_low(w[0]);
+    v[4 * j + 1] += bf16_high(w[0]);
+    v[4 * j + 2] += bf16_low(w[1]);
+    v[4 * j + 3] += bf16_high(w[1]);
 }
 
 template <Product kP, bool kGated, int kAct>
 __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmParams p) {
+    constexpr bool kWg = kP == Product::kWeightGrad;
     constexpr bool kATc = kP != Product::kWeightGrad;  // x, d_z rows: T-contiguous
     constexpr bool kBTc = kP == Product::kForward;     // w rows
     constexpr int kColsPerTile = kGated ? kTileCols / 2 : kTileCols;
     __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
-    __shared__ int64_t pre_s[kMaxExperts + 1];
+    __shared__ int64_t pre_s[kMaxExperts + 1], off_s[kMaxExperts + 1];
     __shared__ int64_t part[kTileThreads / 64];
     const int64_t cols = kP == Product::kForward ? p.n : p.k;
     const int64_t col_tiles = (cols + kColsPerTile - 1) / kColsPerTile;
+    for (int i = threadIdx.x; i <= p.num_experts; i += kTileThreads) off_s[i] = p.off[i];
     const bool ok = expert_items<kTileThreads>(p.off, p.num_experts, p.max_rows, pre_s, part, [&](int64_t rows) {
-        const int64_t r = kP == Product::kWeightGrad ? p.m : rows;
+        const int64_t r = kWg ? p.m : rows;
         return (r + kTileRows - 1) / kTileRows * col_tiles;
     });
     if (!ok) return;
@@ -85,152 +135,136 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
     // serves neighbouring tiles.
     const int64_t grid = gridDim.x;
     const int64_t slot = (int64_t)(blockIdx.x % kXcdCount) * (grid / kXcdCount) + blockIdx.x / kXcdCount;
-    for (int64_t id = slot; id < total; id += grid) {
-        const int e = expert_of_item(pre_s, p.num_experts, id);
-        const int64_t first = wave_uniform64(p.off[e]), count = wave_uniform64(p.off[e + 1]) - first;
-        const int64_t rows = kP == Product::kWeightGrad ? p.m : count;
-        // Groups of kGroupRows row tiles, within a group row tiles fastest; a
-        // remainder of up to three joins the last group (it would stream every
-        // column tile again for itself).
-        const int64_t local = id - wave_uniform64(pre_s[e]);
-        const int64_t mt = (rows + kTileRows - 1) / kTileRows;
-        const int64_t groups = mt % kGroupRows <= 3 && mt >= kGroupRows ? mt / kGroupRows : (mt + kGroupRows - 1) / kGroupRows;
-        const int64_t g0 = local / (kGroupRows * col_tiles), g = g0 < groups - 1 ? g0 : groups - 1;
-        const int64_t gsize = g == groups - 1 ? mt - g * kGroupRows : kGroupRows;
-        const int64_t in_group = local - g * kGroupRows * col_tiles;
-        const int64_t r0 = wave_uniform64((g * kGroupRows + in_group % gsize) * kTileRows);
-        const int64_t c0 = wave_uniform64(in_group / gsize * kColsPerTile);
-        const int64_t rows_left = rows - r0 < kTileRows ? rows - r0 : kTileRows;
-        const int64_t cols_left = cols - c0 < kColsPerTile ? cols - c0 : kColsPerTile;
-
-        OperandView a{}, b{};
-        int a_row = wave * 16, b_row = wave * 16;
-        uint32_t a_half, b_half;
+    // The operands of a tile.
+    auto operands_of = [&](const TileCoord& t) __attribute__((always_inline)) {
+        TileOperands o{};
+        const int64_t rows_left = (kWg ? p.m : t.count) - t.r0, cols_left = cols - t.c0;
+        const int64_t extent_a = rows_left < kTileRows ? rows_left : kTileRows;
+        const int64_t extent_b = cols_left < kColsPerTile ? cols_left : kColsPerTile;
+        o.a_row = o.b_row = wave * 16;
         if constexpr (kP == Product::kForward) {
-            a.first = reinterpret_cast<const char*>(p.a + (first + r0) * p.k);
-            a.rows_bytes = b.rows_bytes = p.k * 2;
-            a.depth = b.depth = p.k;
-            a.extent = rows_left;
-            b.extent = cols_left;
+            o.a.first = reinterpret_cast<const char*>(p.a + (t.first + t.r0) * p.k);
+            o.a.rows_bytes = o.b.rows_bytes = p.k * 2;
+            o.a.depth = o.b.depth = p.k;
+            o.a.extent = extent_a;
+            o.b.extent = extent_b;
             const bool up = kGated && wave % 4 >= 2;  // which rows of w this wave loads
-            if constexpr (kGated) b_row = wave / 4 * 32 + wave % 2 * 16;
-            b.first = reinterpret_cast<const char*>(p.b + ((int64_t)e * p.m + (up ? p.n : 0) + c0) * p.k);
-            a_half = (uint32_t)(128 * a.rows_bytes);
-            b_half = (uint32_t)((kGated ? 64 : 128) * b.rows_bytes);
+            if constexpr (kGated) o.b_row = wave / 4 * 32 + wave % 2 * 16;
+            o.b.first = reinterpret_cast<const char*>(p.b + ((int64_t)t.expert * p.m + (up ? p.n : 0) + t.c0) * p.k);
+            o.a_half = (uint32_t)(128 * o.a.rows_bytes);
+            o.b_half = (uint32_t)((kGated ? 64 : 128) * o.b.rows_bytes);
         } else if constexpr (kP == Product::kInputGrad) {
-            a.first = reinterpret_cast<const char*>(p.a + (first + r0) * p.m);
-            a.rows_bytes = p.m * 2;
-            a.depth = b.depth = p.m;
-            a.extent = rows_left;
-            b.first = reinterpret_cast<const char*>(p.b + (int64_t)e * p.m * p.k + c0);
-            b.rows_bytes = p.k * 2;
-            b.col_bytes = c0 * 2;
-            b_row = wave * 8;
-            a_half = (uint32_t)(128 * a.rows_bytes);
-            b_half = 256;
+            o.a.first = reinterpret_cast<const char*>(p.a + (t.first + t.r0) * p.m);
+            o.a.rows_bytes = p.m * 2;
+            o.a.depth = o.b.depth = p.m;
+            o.a.extent = extent_a;
+            o.b.first = reinterpret_cast<const char*>(p.b + (int64_t)t.expert * p.m * p.k + t.c0);
+            o.b.rows_bytes = p.k * 2;
+            o.b.col_bytes = t.c0 * 2;
+            o.b_row = wave * 8;
+            o.a_half = (uint32_t)(128 * o.a.rows_bytes);
+            o.b_half = 256;
         } else {
-            a.first = reinterpret_cast<const char*>(p.a + first * p.m + r0);
-            b.first = reinterpret_cast<const char*>(p.b + first * p.k + c0);
-            a.rows_bytes = p.m * 2;
-            b.rows_bytes = p.k * 2;
-            a.col_bytes = r0 * 2;
-            b.col_bytes = c0 * 2;
-            a.depth = b.depth = count;
-            a_row = b_row = wave * 8;
-            a_half = b_half = 256;
+            o.a.first = reinterpret_cast<const char*>(p.a + t.first * p.m + t.r0);
+            o.b.first = reinterpret_cast<const char*>(p.b + t.first * p.k + t.c0);
+            o.a.rows_bytes = p.m * 2;
+            o.b.rows_bytes = p.k * 2;
+            o.a.col_bytes = t.r0 * 2;
+            o.b.col_bytes = t.c0 * 2;
+            o.a.depth = o.b.depth = t.count;
+            o.a_row = o.b_row = wave * 8;
+            o.a_half = o.b_half = 256;
         }
+        return o;
+    };
+    auto coord_of = [&](int64_t id) __attribute__((always_inline)) {
+        return tile_coord<kWg>(id, pre_s, off_s, p.num_experts, p.m, col_tiles, kColsPerTile);
+    };
+    // Stores of every tile at least (vectors of its outputs, per lane).
+    constexpr int kStores = kGated ? 8 : 16;
+
+    if (slot >= total) return;
+    TileCoord next = coord_of(slot);
+    TileOperands ops = operands_of(next);
+    begin_tile<kATc, kBTc>(lds, ops);
+    for (int64_t id = slot; id < total; id += grid) {
+        const TileCoord t = next;
+        const bool more = id + grid < total;
+        const int64_t rows_left = (kWg ? p.m : t.count) - t.r0;
         TileSums sums;
-        tile_sums<kATc, kBTc>(lds, a, b, a_row, b_row, a_half, b_half, sums);
+        clear_sums(sums);
+        if (more) next = coord_of(id + grid);  // while the first loads are under way
+        tile_sums<kATc, kBTc, kStores>(lds, ops, id == slot, rows_left > 128, sums);
+        // The next tile's first loads go out ahead of this tile's stores and
+        // land while the results are worked out.
+        if (more) {
+            ops = operands_of(next);
+            begin_tile<kATc, kBTc>(lds, ops);
+        }
 
         const int lane = opaque_lane();
-        const int64_t row0 = (kP == Product::kWeightGrad ? (int64_t)e * p.m : first) + r0;
-        const int rl = (int)rows_left, cl = (int)cols_left;
+        const int64_t row0 = (kWg ? (int64_t)t.expert * p.m : t.first) + t.r0;
+        const int rl = (int)(rows_left < kTileRows ? rows_left : kTileRows);
+        const int cl = (int)(cols - t.c0 < kColsPerTile ? cols - t.c0 : kColsPerTile);
         if constexpr (kGated) {
-            using Out = StagedTile<kTileCols / 2>;
-            // gate and up go out first, as they are; h after them
             if (p.pre != nullptr) {
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    char* half = lds + g * (kTileLds / 2);
-                    for_each_run(sums, g, wm, lane,
-                                 [&](int r, int c, const float(&v)[4]) { Out::put(half, r, wn * 32 + c, v); });
-                }
-                lds_phase_barrier();
-                Out::store(lds, p.pre + row0 * p.m + c0, p.m, rl, cl, wave, lane);
-                Out::store(lds + kTileLds / 2, p.pre + row0 * p.m + p.n + c0, p.m, rl, cl, wave, lane);
-                lds_phase_barrier();
+                const TileMatrix gate(p.pre + row0 * p.m + t.c0, p.m, t.c0, rl, cl);
+                const TileMatrix up(p.pre + row0 * p.m + p.n + t.c0, p.m, p.n + t.c0, rl, cl);
+                for_each_pair(wm, lane, [&](int h, int f, int q, int r, int c) {
+                    gate.store(r, wn * 32 + c, pack_pair(sums.v[h][f][0], q));
+                    up.store(r, wn * 32 + c, pack_pair(sums.v[h][f][1], q));
+                });
             }
+            const TileMatrix out(p.out + row0 * p.n + t.c0, p.n, t.c0, rl, cl);
+            for_each_pair(wm, lane, [&](int h, int f, int q, int r, int c) {
+                f32x16& v = sums.v[h][f][0];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sums.v[h][f][0][i] = act_value<kAct>(sums.v[h][f][0][i]) * sums.v[h][f][1][i];
-            for_each_run(sums, 0, wm, lane,
-                         [&](int r, int c, const float(&v)[4]) { Out::put(lds, r, wn * 32 + c, v); });
-            lds_phase_barrier();
-            Out::store(lds, p.out + row0 * p.n + c0, p.n, rl, cl, wave, lane);
+                for (int i = 8 * q; i < 8 * q + 8; ++i) v[i] = act_value<kAct>(v[i]) * sums.v[h][f][1][i];
+                out.store(r, wn * 32 + c, pack_pair(v, q));
+            });
         } else {
-            using Out = StagedTile<kTileCols>;
-            uint16_t* out = p.out + row0 * cols + c0;
+            const TileMatrix out(p.out + row0 * cols + t.c0, cols, t.c0, rl, cl);
             if constexpr (kP == Product::kForward) {
-                if (p.bias != nullptr) {
+                const TileMatrix pre(p.pre + row0 * p.n + t.c0, p.n, t.c0, rl, cl);
+                const TileMatrix res(p.residual + row0 * p.n + t.c0, p.n, t.c0, rl, cl);
 #pragma unroll
-                    for (int cb = 0; cb < 2; ++cb)
+                for (int cb = 0; cb < 2; ++cb) {
+                    const int col = wn * 64 + cb * 32;
+                    if (p.bias != nullptr) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int c = wn * 64 + cb * 32 + j * 8 + lane / 32 * 4;
+                            const int c = col + j * 8 + lane / 32 * 4;
                             u32x2 bv = {0u, 0u};
-                            if (c < cl) bv = *reinterpret_cast<const u32x2*>(p.bias + (int64_t)e * p.n + c0 + c);
-                            const float bias[4] = {bf16_low(bv[0]), bf16_high(bv[0]), bf16_low(bv[1]), bf16_high(bv[1])};
+                            if (c < cl) bv = *reinterpret_cast<const u32x2*>(p.bias + t.expert * p.n + t.c0 + c);
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                                    for (int q = 0; q < 4; ++q) sums.v[h][f][cb][4 * j + q] += bias[q];
+                                for (int f = 0; f < 2; ++f) add4(sums.v[h][f][cb], j, bv);
                         }
-                }
-                if (p.pre != nullptr) {
-#pragma unroll
-                    for (int cb = 0; cb < 2; ++cb)
-                        for_each_run(sums, cb, wm, lane, [&](int r, int c, const float(&v)[4]) {
-                            Out::put(lds, r, wn * 64 + cb * 32 + c, v);
-                        });
-                    lds_phase_barrier();
-                    Out::store(lds, p.pre + row0 * p.n + c0, p.n, rl, cl, wave, lane);
-                    lds_phase_barrier();
-                }
-                if (p.residual != nullptr) {
-                    // the residual's tile, where the result will stand
-                    Out::load(lds, p.residual + row0 * p.n + c0, p.n, rl, wave, lane, c0 * 2);
-                    wait_loads<0>();
-                    lds_phase_barrier();
-                }
-            }
-#pragma unroll
-            for (int cb = 0; cb < 2; ++cb)
-                for_each_run(sums, cb, wm, lane, [&](int r, int c, const float(&v)[4]) {
-                    const int col = wn * 64 + cb * 32 + c;
-                    if constexpr (kP == Product::kForward) {
-                        float y[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) y[q] = act_value<kAct>(v[q]);
-                        if (p.residual != nullptr) {
-                            const u32x2 rv = *Out::at(lds, r, col);
-                            y[0] += bf16_low(rv[0]), y[1] += bf16_high(rv[0]);
-                            y[2] += bf16_low(rv[1]), y[3] += bf16_high(rv[1]);
-                        }
-                        Out::put(lds, r, col, y);
-                    } else {
-                        Out::put(lds, r, col, v);
                     }
-                });
-            lds_phase_barrier();
-            Out::store(lds, out, cols, rl, cl, wave, lane);
+                    for_each_pair(wm, lane, [&](int h, int f, int q, int r, int c) {
+                        f32x16& v = sums.v[h][f][cb];
+                        if (p.pre != nullptr) pre.store(r, col + c, pack_pair(v, q));
+#pragma unroll
+                        for (int i = 8 * q; i < 8 * q + 8; ++i) v[i] = act_value<kAct>(v[i]);
+                        if (p.residual != nullptr) {
+                            u32x2 even, odd;
+                            vector_to_runs(res.load(r, col + c), even, odd);
+                            add4(v, 2 * q, even);
+                            add4(v, 2 * q + 1, odd);
+                        }
+                        out.store(r, col + c, pack_pair(v, q));
+                    });
+                }
+            } else {
+#pragma unroll
+                for (int cb = 0; cb < 2; ++cb)
+                    for_each_pair(wm, lane, [&](int h, int f, int q, int r, int c) {
+                        out.store(r, wn * 64 + cb * 32 + c, pack_pair(sums.v[h][f][cb], q));
+                    });
+            }
         }
-        lds_phase_barrier();  // the stages are free for the next tile
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 

@@ -238,135 +238,169 @@ __device__ __forceinline__ void multiply(const Frags& a, const Frags& b, f32x16 
     __builtin_amdgcn_s_setprio(0);
 }
 
-// The k-loop of one tile.  a_row / b_row: this wave's first row of its loads
-// of a half tile; a_half / b_half: byte offset of the second half tile.  On
-// entry every wave is past its LDS use of the tile before; on return no load
-// is in flight and every wave is done with LDS (one barrier included).
-template <bool kATc, bool kBTc>
-__device__ __forceinline__ void tile_sums(char* lds, const OperandView& a, const OperandView& b, int a_row, int b_row,
-                                          uint32_t a_half, uint32_t b_half, TileSums& sums) {
-    const int lane = opaque_lane();
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int wm = wave / 4, wn = wave % 4;
-    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-    const uint32_t a_voff[2] = {load_offset<kATc>(a.rows_bytes, a_row, lane, 0),
-                                load_offset<kATc>(a.rows_bytes, a_row, lane, 1)};
-    const uint32_t b_voff[2] = {load_offset<kBTc>(b.rows_bytes, b_row, lane, 0),
-                                load_offset<kBTc>(b.rows_bytes, b_row, lane, 1)};
-    const uint32_t a_frag = lds0 + kPartA * kHalfBytes + frag_offset<kATc>(wm, lane);
-    const uint32_t b_frag = lds0 + (kPartB + wn / 2) * kHalfBytes + frag_offset<kBTc>(wn % 2, lane);
-    const int64_t steps = (a.depth + kStepT - 1) / kStepT;
+// The two operands of a tile, as this wave loads and reads them: a_row / b_row
+// are its first stored row in a half tile, a_half / b_half the byte offset of
+// the second half tile.
+struct TileOperands {
+    OperandView a, b;
+    int a_row, b_row;
+    uint32_t a_half, b_half;
+};
 
-    auto load_b_a0 = [&](int64_t step) __attribute__((always_inline)) {
+template <bool kATc, bool kBTc>
+struct TileLoader {
+    char* lds;
+    const TileOperands& o;
+    uint32_t a_voff[2], b_voff[2];
+    int wave, lane;
+
+    __device__ __forceinline__ TileLoader(char* lds_, const TileOperands& o_) : lds(lds_), o(o_) {
+        lane = opaque_lane();
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            a_voff[i] = load_offset<kATc>(o.a.rows_bytes, o.a_row, lane, i);
+            b_voff[i] = load_offset<kBTc>(o.b.rows_bytes, o.b_row, lane, i);
+        }
+    }
+    __device__ __forceinline__ void b_a0(int64_t step) const {
         char* stage = lds + (step % 2) * kStageBytes;
         int rem;
-        const __amdgpu_buffer_rsrc_t rb = step_resource<kBTc>(b, step, rem);
+        const __amdgpu_buffer_rsrc_t rb = step_resource<kBTc>(o.b, step, rem);
         load_half<kBTc>(stage + kPartB * kHalfBytes, rb, b_voff, 0, rem, wave, lane);
-        load_half<kBTc>(stage + (kPartB + 1) * kHalfBytes, rb, b_voff, b_half, rem, wave, lane);
-        const __amdgpu_buffer_rsrc_t ra = step_resource<kATc>(a, step, rem);
+        load_half<kBTc>(stage + (kPartB + 1) * kHalfBytes, rb, b_voff, o.b_half, rem, wave, lane);
+        const __amdgpu_buffer_rsrc_t ra = step_resource<kATc>(o.a, step, rem);
         load_half<kATc>(stage + kPartA * kHalfBytes, ra, a_voff, 0, rem, wave, lane);
-    };
-    auto load_a1 = [&](int64_t step) __attribute__((always_inline)) {
+    }
+    __device__ __forceinline__ void a1(int64_t step) const {
         int rem;
-        const __amdgpu_buffer_rsrc_t ra = step_resource<kATc>(a, step, rem);
-        load_half<kATc>(lds + (step % 2) * kStageBytes + (kPartA + 1) * kHalfBytes, ra, a_voff, a_half, rem, wave,
+        const __amdgpu_buffer_rsrc_t ra = step_resource<kATc>(o.a, step, rem);
+        load_half<kATc>(lds + (step % 2) * kStageBytes + (kPartA + 1) * kHalfBytes, ra, a_voff, o.a_half, rem, wave,
                         lane);
-    };
+    }
+};
 
+// The first loads of a tile: B and A0 of step 0 (6), A1 of step 0 (2), B and A0
+// of step 1 (6).  Every wave must be done with LDS.
+template <bool kATc, bool kBTc>
+__device__ __forceinline__ void begin_tile(char* lds, const TileOperands& o) {
+    const TileLoader<kATc, kBTc> load(lds, o);
+    load.b_a0(0);
+    load.a1(0);
+    load.b_a0(1);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+__device__ __forceinline__ void clear_sums(TileSums& sums) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int f = 0; f < 2; ++f)
 #pragma unroll
             for (int c = 0; c < 2; ++c) sums.v[h][f][c] = f32x16{};
+}
 
-    load_b_a0(0);
-    load_a1(0);
-    load_b_a0(1);
-    wait_loads<8>();           // B and A0 of step 0; A1 of step 0 (2) and B, A0 of step 1 (6) stay in flight
+// The k-loop of a tile whose first loads are under way (begin_tile).  kStores:
+// vector-memory operations that this wave issued after them, at least (the
+// stores of the tile before; they need not be waited for until step 1);
+// `fresh`: none were.  second_half: the tile has rows in its second half (the
+// barriers are the same without; its reads and MFMAs are left out).  On return
+// no load is in flight and every wave is done with LDS.
+template <bool kATc, bool kBTc, int kStores>
+__device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool fresh, bool second_half,
+                                          TileSums& sums) {
+    static_assert(8 + kStores < 64, "vector-memory counter range");
+    const TileLoader<kATc, kBTc> load(lds, o);
+    const int lane = load.lane, wm = load.wave / 4, wn = load.wave % 4;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+    const uint32_t a_frag = lds0 + kPartA * kHalfBytes + frag_offset<kATc>(wm, lane);
+    const uint32_t b_frag = lds0 + (kPartB + wn / 2) * kHalfBytes + frag_offset<kBTc>(wn % 2, lane);
+    const int64_t steps = (o.a.depth + kStepT - 1) / kStepT;
+
+    __builtin_amdgcn_sched_barrier(0);
+    if (fresh) wait_loads<0>();
+    else wait_loads<8 + kStores>();  // B and A0 of step 0; A1 (2), B and A0 of step 1 (6) and the stores stay in flight
     phase_barrier();
-    if (wm == 1) phase_barrier();  // the second row of waves runs one interval behind
-    Frags fa, fb;
-    for (int64_t step = 0; step < steps; ++step) {
-        const uint32_t stage = (uint32_t)(step % 2) * kStageBytes;
-        load_a1(step + 1);
-        read_frags<kBTc>(b_frag + stage, fb);
-        read_frags<kATc>(a_frag + stage, fa);
-        wait_loads<8>();       // A1 of this step; B, A0 (6) and A1 (2) of the next stay in flight
-        phase_barrier();
-        multiply(fa, fb, sums.v[0]);
-        phase_barrier();
-        load_b_a0(step + 2);   // into this stage: every wave has read its B and A0
-        read_frags<kATc>(a_frag + stage + kHalfBytes, fa);
-        wait_loads<8>();       // B and A0 of the next step; its A1 (2) and B, A0 of the one after (6) stay in flight
-        phase_barrier();
-        multiply(fa, fb, sums.v[1]);
-        phase_barrier();
-    }
+    if (wm == 1) phase_barrier();    // the second row of waves runs one interval behind
+
+    auto run = [&](auto tag) __attribute__((always_inline)) {
+        constexpr bool kBoth = decltype(tag)::value != 0;
+        auto one_step = [&](int64_t step, auto extra) __attribute__((always_inline)) {
+            constexpr int kExtra = decltype(extra)::value;
+            Frags fa, fb;
+            const uint32_t stage = (uint32_t)(step % 2) * kStageBytes;
+            load.a1(step + 1);
+            read_frags<kBTc>(b_frag + stage, fb);
+            read_frags<kATc>(a_frag + stage, fa);
+            wait_loads<8 + kExtra>();  // A1 of this step; B, A0 (6) and A1 (2) of the next stay in flight
+            phase_barrier();
+            multiply(fa, fb, sums.v[0]);
+            phase_barrier();
+            load.b_a0(step + 2);       // into this stage: every wave has read its B and A0
+            if constexpr (kBoth) read_frags<kATc>(a_frag + stage + kHalfBytes, fa);
+            wait_loads<8 + kExtra>();  // B, A0 of the next step; its A1 (2) and the B, A0 after (6) stay in flight
+            phase_barrier();
+            if constexpr (kBoth) multiply(fa, fb, sums.v[1]);
+            phase_barrier();
+        };
+        if (steps > 0) one_step(0, ActTag<kStores>{});
+        for (int64_t step = 1; step < steps; ++step) one_step(step, ActTag<0>{});
+    };
+    if (second_half) run(ActTag<1>{});
+    else run(ActTag<0>{});
     if (wm == 0) phase_barrier();
     wait_loads<0>();
     phase_barrier();
 }
 
-// Barrier around the epilogue's use of LDS: this wave's LDS accesses are done
-// before it arrives; stores in flight are not waited for.
-__device__ __forceinline__ void lds_phase_barrier() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
+// Two of a lane's runs of four consecutive outputs, 8 columns apart (columns
+// 16 p + 4 (l / 32) .. and 16 p + 8 + 4 (l / 32) ..), and one 16-byte vector of
+// eight consecutive columns, 16 p + 8 (l / 32) ..: the halves of the wave
+// exchange a run each.  v_permlane32_swap_b32 swaps the upper half of its
+// first register with the lower half of its second; it is its own inverse.
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ u32x4 runs_to_vector(u32x2 even, u32x2 odd) {
+    uint32_t e0 = even[0], e1 = even[1], o0 = odd[0], o1 = odd[1];
+    swap_halves(e0, o0);
+    swap_halves(e1, o1);
+    return u32x4{e0, e1, o0, o1};
+}
+__device__ __forceinline__ void vector_to_runs(u32x4 v, u32x2& even, u32x2& odd) {
+    uint32_t e0 = v[0], e1 = v[1], o0 = v[2], o1 = v[3];
+    swap_halves(e0, o0);
+    swap_halves(e1, o1);
+    even = u32x2{e0, e1};
+    odd = u32x2{o0, o1};
 }
 
-// A finished tile in LDS: 256 rows of kCols bf16, the 16-byte units of a row
-// XOR-swizzled by the row so that the 16 rows of an 8-byte write's phase touch
-// different banks.  Results go out through it as whole rows: stored straight
-// from the MFMA layout, an instruction writes 16 bytes of each of 32 rows, and
-// those partial lines cost more than the product of a short T (see below).
-template <int kCols>
-struct StagedTile {
-    static constexpr int kUnits = kCols / 8, kPitch = kCols * 2;
-    static constexpr int kRowsPerLoad = 1024 / kPitch, kInstr = kTileRows / 8 / kRowsPerLoad;
-    static_assert(kTileRows * kPitch <= kTileLds, "a staged tile fits the stages");
+// A tile's rows and columns in a row-major bf16 matrix, as a buffer resource:
+// vectors past its rows or columns are not stored and read as zero, so every
+// tile issues the same operations.
+struct TileMatrix {
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t row_bytes;
+    int cols;
 
-    // Address of columns col .. col + 3 (col a multiple of 4) of a row.
-    static __device__ __forceinline__ u32x2* at(char* lds, int row, int col) {
-        return reinterpret_cast<u32x2*>(lds + row * kPitch + ((col / 8) ^ (row % kUnits)) * 16 + col % 8 * 2);
+    // first: the tile's first element, col0 columns into a row of `stride`.
+    __device__ __forceinline__ TileMatrix(const uint16_t* first, int64_t stride, int64_t col0, int rows, int cols_) {
+        rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)wave_uniform64((int64_t)first), 0,
+                                                 __builtin_amdgcn_readfirstlane((int)((rows * stride - col0) * 2)),
+                                                 0x00020000);
+        row_bytes = (uint32_t)(stride * 2);
+        cols = cols_;
     }
-    static __device__ __forceinline__ void put(char* lds, int row, int col, const float (&v)[4]) {
-        *at(lds, row, col) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    __device__ __forceinline__ int offset(int row, int col) const {
+        return (int)(col < cols ? (uint32_t)row * row_bytes + (uint32_t)col * 2 : kOutOfRange);
     }
-    // Row and 16-byte unit of this lane in instruction i of its wave.
-    static __device__ __forceinline__ int lane_row(int wave, int lane, int i) {
-        return wave * (kTileRows / 8) + i * kRowsPerLoad + lane / kUnits;
+    __device__ __forceinline__ void store(int row, int col, u32x4 v) const {
+        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, offset(row, col), 0, 0);
     }
-    // The whole tile (after a barrier) to dst, rows `stride` elements apart.
-    static __device__ __forceinline__ void store(const char* lds, uint16_t* dst, int64_t stride, int rows, int cols,
-                                                 int wave, int lane) {
-        u32x4 v[kInstr];
-        const int unit = lane % kUnits;
-#pragma unroll
-        for (int i = 0; i < kInstr; ++i) {
-            const int r = lane_row(wave, lane, i);
-            v[i] = *reinterpret_cast<const u32x4*>(lds + r * kPitch + (unit ^ (r % kUnits)) * 16);
-        }
-#pragma unroll
-        for (int i = 0; i < kInstr; ++i) {
-            const int r = lane_row(wave, lane, i);
-            if (r < rows && unit * 8 < cols) *reinterpret_cast<u32x4*>(dst + r * stride + unit * 8) = v[i];
-        }
-    }
-    // The whole tile from src straight into LDS; waited for by the caller.
-    static __device__ __forceinline__ void load(char* lds, const uint16_t* src, int64_t stride, int rows, int wave,
-                                                int lane, int64_t col_bytes) {
-        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)wave_uniform64((int64_t)src), 0,
-            __builtin_amdgcn_readfirstlane((int)(rows * stride * 2 - col_bytes)), 0x00020000);
-#pragma unroll
-        for (int i = 0; i < kInstr; ++i) {
-            const int r = lane_row(wave, lane, i);
-            const int off = (int)(r * stride * 2) + ((lane % kUnits) ^ (r % kUnits)) * 16;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * kInstr + i) * 1024), 16, off, 0, 0, 0);
-        }
+    __device__ __forceinline__ u32x4 load(int row, int col) const {
+        return __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset(row, col), 0, 0);
     }
 };
 
