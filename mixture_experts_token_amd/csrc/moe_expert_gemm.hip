@@ -293,6 +293,7 @@ GemmParams params_of(const ExpertRows& rows, int64_t m, int64_t k, const void* a
 }  // namespace
 
 hipError_t launch_expert_forward(const ExpertForwardArgs& a, int num_cus, hipStream_t stream) {
+    if (expert_stream_applies(a)) return launch_expert_stream(a, num_cus, stream);
     GemmParams p = params_of(a.rows, a.gated ? 2 * a.n : a.n, a.k, a.x, a.w, a.y);
     p.n = a.n;
     p.bias = static_cast<const uint16_t*>(a.bias);

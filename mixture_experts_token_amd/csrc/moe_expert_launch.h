@@ -77,6 +77,9 @@ struct UnpermuteBackwardArgs {
 };
 
 hipError_t launch_expert_forward(const ExpertForwardArgs& a, int num_cus, hipStream_t stream);
+// The forward for experts with few rows each (called by launch_expert_forward where it applies).
+bool expert_stream_applies(const ExpertForwardArgs& a);
+hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, hipStream_t stream);
 hipError_t launch_expert_input_grad(const ExpertInputGradArgs& a, int num_cus, hipStream_t stream);
 hipError_t launch_expert_weight_grad(const ExpertWeightGradArgs& a, int num_cus, hipStream_t stream);
 hipError_t launch_expert_act_grad(const ExpertActGradArgs& a, int num_cus, hipStream_t stream);

@@ -64,6 +64,9 @@ SHAPES = [
     ([17, 5, 9, 33], 1032, 448),
     ([300] + [0] * 30 + [5], 128, 128),
     ([1] * 1024, 40, 64),
+    ([9, 1, 3, 8, 0, 4], 72, 1096),
+    ([0, 5, 1], 136, 16392),
+    ([2, 0, 1], 40, 33000),
 ]
 ACTS = ["silu", "gelu_tanh", "relu", "none"]
 
