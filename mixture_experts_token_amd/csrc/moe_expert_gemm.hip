@@ -26,7 +26,7 @@ namespace moe {
 
 namespace {
 
-enum class Product { kForward, kInputGrad, kWeightGrad };
+enum class Product { kForward, kInputGrad, kWeightGrad, kWeightBiasGrad };
 
 constexpr int kXcdCount = 8;
 constexpr int64_t kGroupRows = 8;  // row tiles per group in the tile order
@@ -42,6 +42,7 @@ struct GemmParams {
     const uint16_t* bias;
     const uint16_t* residual;
     uint16_t* pre;
+    uint16_t* d_bias;          // [num_experts, m] (weight and bias grad)
     uint16_t* out;
 };
 
@@ -112,8 +113,9 @@ __device__ __forceinline__ void add4(f32x16& v, int j, u32x2 w) {
 
 template <Product kP, bool kGated, int kAct>
 __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmParams p) {
-    constexpr bool kWg = kP == Product::kWeightGrad;
-    constexpr bool kATc = kP != Product::kWeightGrad;  // x, d_z rows: T-contiguous
+    constexpr bool kBiasGrad = kP == Product::kWeightBiasGrad;
+    constexpr bool kWg = kP == Product::kWeightGrad || kBiasGrad;
+    constexpr bool kATc = !kWg;                        // x, d_z rows: T-contiguous
     constexpr bool kBTc = kP == Product::kForward;     // w rows
     constexpr int kColsPerTile = kGated ? kTileCols / 2 : kTileCols;
     __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
@@ -194,7 +196,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
         TileSums sums;
         clear_sums(sums);
         if (more) next = coord_of(id + grid);  // while the first loads are under way
-        tile_sums<kATc, kBTc, kStores>(lds, ops, id == slot, rows_left > 128, sums);
+        tile_sums<kATc, kBTc, kStores, kBiasGrad>(lds, ops, id == slot, rows_left > 128, sums);
         // The next tile's first loads go out ahead of this tile's stores and
         // land while the results are worked out.
         if (more) {
@@ -264,6 +266,20 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
                     });
             }
         }
+        if constexpr (kBiasGrad) {
+            // d_z's column sums are the sums of operand a: the first column
+            // tile's first waves hold them, half of T in lanes l and l + 32.
+            if (t.c0 == 0 && wn == 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const float lo = sums.a_sum[h][f], sum = lo + __shfl_xor(lo, 32, 64);
+                        const int r = h * 128 + wm * 64 + f * 32 + lane;
+                        if (lane < 32 && r < rl) p.d_bias[row0 + r] = (uint16_t)pack_bf16(sum, 0.0f);
+                    }
+            }
+        }
         __builtin_amdgcn_sched_barrier(0);
     }
 }
@@ -312,8 +328,10 @@ hipError_t launch_expert_input_grad(const ExpertInputGradArgs& a, int num_cus, h
 }
 
 hipError_t launch_expert_weight_grad(const ExpertWeightGradArgs& a, int num_cus, hipStream_t stream) {
-    return launch_product<Product::kWeightGrad, false, kActNone>(params_of(a.rows, a.m, a.k, a.d_z, a.x, a.d_w),
-                                                                 num_cus, stream);
+    GemmParams p = params_of(a.rows, a.m, a.k, a.d_z, a.x, a.d_w);
+    p.d_bias = static_cast<uint16_t*>(a.d_bias);
+    return p.d_bias != nullptr ? launch_product<Product::kWeightBiasGrad, false, kActNone>(p, num_cus, stream)
+                               : launch_product<Product::kWeightGrad, false, kActNone>(p, num_cus, stream);
 }
 
 }  // namespace moe

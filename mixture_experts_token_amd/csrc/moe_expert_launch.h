@@ -37,13 +37,14 @@ struct ExpertInputGradArgs {
     void* d_x;                  // [max_rows, k]
 };
 
-// d_w[e] = d_z[rows of e]^T x[rows of e].
+// d_w[e] = d_z[rows of e]^T x[rows of e], and with d_bias the sums of d_z's rows.
 struct ExpertWeightGradArgs {
     ExpertRows rows;
     int64_t m, k;
     const void* d_z;            // [max_rows, m]
     const void* x;              // [max_rows, k]
     void* d_w;                  // [num_experts, m, k]
+    void* d_bias;               // [num_experts, m] or null
 };
 
 // d_z = d_y * act'(pre), or with `gated` both projections' gradient from d_h and gate_up.
@@ -57,6 +58,7 @@ struct ExpertActGradArgs {
     void* d_z;
 };
 
+// The bias gradient alone (a weight gradient takes it along).
 struct ExpertBiasGradArgs {
     ExpertRows rows;
     int64_t n;

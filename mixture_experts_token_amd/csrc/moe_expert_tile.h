@@ -222,19 +222,37 @@ __device__ __forceinline__ void read_frags(uint32_t a, Frags& fr) {
 // The tile's sums: half h, row block f, column block c of this wave.  Lane l,
 // register 4 j + q holds row 128 h + 64 wm + 32 f + l % 32, column
 // 64 wn + 32 c + 8 j + 4 (l / 32) + q (the MFMA takes the column operand first).
+// a_sum: with kSumA, row 128 h + 64 wm + 32 f + l % 32 of operand a summed over
+// the T that lane l's fragments hold (the other half of them is in lane l ^ 32).
 struct TileSums {
     f32x16 v[2][2][2];
+    float a_sum[2][2];
 };
 
-__device__ __forceinline__ void multiply(const Frags& a, const Frags& b, f32x16 (&acc)[2][2]) {
+template <bool kSumA>
+__device__ __forceinline__ void multiply(const Frags& a, const Frags& b, f32x16 (&acc)[2][2], float (&a_sum)[2]) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 4; ++s) {
 #pragma unroll
         for (int f = 0; f < 2; ++f)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
                 acc[f][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[c][s], a.v[f][s], acc[f][c], 0, 0, 0);
+        if constexpr (kSumA) {  // on the vector units, while the matrix cores work
+            const uint32_t ones = 0x3F803F80u;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const u32x4 w = __builtin_bit_cast(u32x4, a.v[f][s]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t wq = w[q];
+                    a_sum[f] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, wq),
+                                                               __builtin_bit_cast(bf16x2, ones), a_sum[f], false);
+                }
+            }
+        }
+    }
     __builtin_amdgcn_s_setprio(0);
 }
 
@@ -297,7 +315,10 @@ __device__ __forceinline__ void clear_sums(TileSums& sums) {
 #pragma unroll
         for (int f = 0; f < 2; ++f)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) sums.v[h][f][c] = f32x16{};
+            for (int c = 0; c < 2; ++c) {
+                sums.v[h][f][c] = f32x16{};
+                sums.a_sum[h][f] = 0.0f;
+            }
 }
 
 // The k-loop of a tile whose first loads are under way (begin_tile).  kStores:
@@ -306,7 +327,7 @@ __device__ __forceinline__ void clear_sums(TileSums& sums) {
 // `fresh`: none were.  second_half: the tile has rows in its second half (the
 // barriers are the same without; its reads and MFMAs are left out).  On return
 // no load is in flight and every wave is done with LDS.
-template <bool kATc, bool kBTc, int kStores>
+template <bool kATc, bool kBTc, int kStores, bool kSumA>
 __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool fresh, bool second_half,
                                           TileSums& sums) {
     static_assert(8 + kStores < 64, "vector-memory counter range");
@@ -334,13 +355,13 @@ __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool
             read_frags<kATc>(a_frag + stage, fa);
             wait_loads<8 + kExtra>();  // A1 of this step; B, A0 (6) and A1 (2) of the next stay in flight
             phase_barrier();
-            multiply(fa, fb, sums.v[0]);
+            multiply<kSumA>(fa, fb, sums.v[0], sums.a_sum[0]);
             phase_barrier();
             load.b_a0(step + 2);       // into this stage: every wave has read its B and A0
             if constexpr (kBoth) read_frags<kATc>(a_frag + stage + kHalfBytes, fa);
             wait_loads<8 + kExtra>();  // B, A0 of the next step; its A1 (2) and the B, A0 after (6) stay in flight
             phase_barrier();
-            if constexpr (kBoth) multiply(fa, fb, sums.v[1]);
+            if constexpr (kBoth) multiply<kSumA>(fa, fb, sums.v[1], sums.a_sum[1]);
             phase_barrier();
         };
         if (steps > 0) one_step(0, ActTag<kStores>{});

@@ -174,9 +174,10 @@ moe_status_t backward_impl(bool gated, const void* d_y, const void* pre, const v
         a.d_z = dz;
         a.x = x;
         a.d_w = d_w;
+        a.d_bias = d_bias;
         if (moe::launch_expert_weight_grad(a, cus, s) != hipSuccess) return MOE_ERR_HIP;
     }
-    if (d_bias != nullptr) {
+    if (d_bias != nullptr && d_w == nullptr) {
         moe::ExpertBiasGradArgs a;
         a.rows = rows;
         a.n = n;

@@ -11,11 +11,10 @@ and a non-OK status raises ``MoEError``.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 from . import binding
-from .binding import MOE_OK, MoEError, _check, _dtype_code, _ptr, _require_gpu, _stream
+from .binding import MOE_OK, MoEError, _dtype_code, _require_gpu
 
 MOE_ACT_NONE = 0
 MOE_ACT_RELU = 1
@@ -57,35 +56,54 @@ def _matrix(t, name: str, dims: int):
     return t
 
 
-def _shaped(t, name: str, shape, device, optional: bool = False) -> None:
-    """A bf16 buffer of exactly this shape."""
-    import torch
+def _buffer(t, name: str, dtypes, shape, device, optional: bool = False):
+    """Raw device address of a contiguous buffer of exactly this shape (None stays None where it may).
 
-    numel = 1
-    for s in shape:
-        numel *= s
-    _check(t, name, (torch.bfloat16,), numel, device, optional=optional)
-    if t is not None and tuple(t.shape) != tuple(shape):
+    One pass over a buffer instead of a check and a conversion: at single
+    tokens the call is as short as its kernel.
+    """
+    if t is None:
+        if optional:
+            return None
+        raise ValueError("%s is required" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if t.shape != shape:
         raise ValueError("%s must be %s, got shape %s" % (name, list(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.device != device:
+        raise TypeError("%s is on %s, expected %s (every buffer of the call on one GPU)" % (name, t.device, device))
+    return t.data_ptr()
 
 
-def _call(name: str, device, stream, tensor, args) -> None:
+def _call(name: str, device, stream, args) -> None:
     """Calls the entry point on the tensors' device, whichever device is current."""
     import torch
 
+    _require_gpu(device)
     if stream is not None and stream.device != device:
         raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
-    other = torch.cuda.current_device() != device.index
-    with torch.cuda.device(device) if other else contextlib.nullcontext():
-        status = getattr(_load(), name)(*args, _stream(stream, tensor))
+    handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    if torch._C._cuda_getDevice() == device.index:
+        status = getattr(_load(), name)(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(_load(), name)(*args, handle)
     if status != MOE_OK:
         raise MoEError(status, name)
 
 
-def _offsets(off, experts: int, device) -> None:
+def _bf16():
     import torch
 
-    _check(off, "expert_first_token_offset", (torch.int64,), experts + 1, device)
+    return (torch.bfloat16,)
+
+
+def _offsets(off, experts: int, device):
+    import torch
+
+    return _buffer(off, "expert_first_token_offset", (torch.int64,), (experts + 1,), device)
 
 
 def _gate_up_width(w):
@@ -107,15 +125,11 @@ def moe_grouped_gated_gemm_bf16(x, w, expert_first_token_offset, h, gate_up=None
     act = _activation(activation)
     experts, n, k = _gate_up_width(w)
     rows = _matrix(x, "x", 2).shape[0]
-    dev = x.device
-    _shaped(x, "x", (rows, k), dev)
-    _shaped(w, "w", (experts, 2 * n, k), dev)
-    _shaped(h, "h", (rows, n), dev)
-    _shaped(gate_up, "gate_up", (rows, 2 * n), dev, optional=True)
-    _offsets(expert_first_token_offset, experts, dev)
-    _require_gpu(dev)
-    _call("moe_grouped_gated_gemm_bf16", dev, stream, x,
-          (_ptr(x), _ptr(w), _ptr(expert_first_token_offset), experts, rows, n, k, act, _ptr(gate_up), _ptr(h)))
+    dev, bf16 = x.device, _bf16()
+    args = (_buffer(x, "x", bf16, (rows, k), dev), _buffer(w, "w", bf16, (experts, 2 * n, k), dev),
+            _offsets(expert_first_token_offset, experts, dev), experts, rows, n, k, act,
+            _buffer(gate_up, "gate_up", bf16, (rows, 2 * n), dev, optional=True), _buffer(h, "h", bf16, (rows, n), dev))
+    _call("moe_grouped_gated_gemm_bf16", dev, stream, args)
 
 
 def moe_grouped_gated_gemm_backward_bf16(d_h, gate_up, x, w, expert_first_token_offset, d_gate_up, d_x=None, d_w=None,
@@ -128,19 +142,14 @@ def moe_grouped_gated_gemm_backward_bf16(d_h, gate_up, x, w, expert_first_token_
     act = _activation(activation)
     experts, n, k = _gate_up_width(w)
     rows = _matrix(d_h, "d_h", 2).shape[0]
-    dev = d_h.device
-    _shaped(d_h, "d_h", (rows, n), dev)
-    _shaped(gate_up, "gate_up", (rows, 2 * n), dev)
-    _shaped(x, "x", (rows, k), dev, optional=d_w is None)
-    _shaped(w, "w", (experts, 2 * n, k), dev)
-    _shaped(d_gate_up, "d_gate_up", (rows, 2 * n), dev)
-    _shaped(d_x, "d_x", (rows, k), dev, optional=True)
-    _shaped(d_w, "d_w", (experts, 2 * n, k), dev, optional=True)
-    _offsets(expert_first_token_offset, experts, dev)
-    _require_gpu(dev)
-    _call("moe_grouped_gated_gemm_backward_bf16", dev, stream, d_h,
-          (_ptr(d_h), _ptr(gate_up), _ptr(x), _ptr(w), _ptr(expert_first_token_offset), experts, rows, n, k, act,
-           _ptr(d_gate_up), _ptr(d_x), _ptr(d_w)))
+    dev, bf16 = d_h.device, _bf16()
+    args = (_buffer(d_h, "d_h", bf16, (rows, n), dev), _buffer(gate_up, "gate_up", bf16, (rows, 2 * n), dev),
+            _buffer(x, "x", bf16, (rows, k), dev, optional=d_w is None),
+            _buffer(w, "w", bf16, (experts, 2 * n, k), dev), _offsets(expert_first_token_offset, experts, dev),
+            experts, rows, n, k, act, _buffer(d_gate_up, "d_gate_up", bf16, (rows, 2 * n), dev),
+            _buffer(d_x, "d_x", bf16, (rows, k), dev, optional=True),
+            _buffer(d_w, "d_w", bf16, (experts, 2 * n, k), dev, optional=True))
+    _call("moe_grouped_gated_gemm_backward_bf16", dev, stream, args)
 
 
 def moe_grouped_linear_bf16(x, w, expert_first_token_offset, y, bias=None, residual=None, pre_activation=None,
@@ -154,18 +163,14 @@ def moe_grouped_linear_bf16(x, w, expert_first_token_offset, y, bias=None, resid
     act = _activation(activation)
     experts, n, k = _matrix(w, "w", 3).shape
     rows = _matrix(x, "x", 2).shape[0]
-    dev = x.device
-    _shaped(x, "x", (rows, k), dev)
-    _shaped(w, "w", (experts, n, k), dev)
-    _shaped(y, "y", (rows, n), dev)
-    _shaped(bias, "bias", (experts, n), dev, optional=True)
-    _shaped(residual, "residual", (rows, n), dev, optional=True)
-    _shaped(pre_activation, "pre_activation", (rows, n), dev, optional=True)
-    _offsets(expert_first_token_offset, experts, dev)
-    _require_gpu(dev)
-    _call("moe_grouped_linear_bf16", dev, stream, x,
-          (_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(expert_first_token_offset), experts, rows, n, k, act,
-           _ptr(pre_activation), _ptr(y)))
+    dev, bf16 = x.device, _bf16()
+    args = (_buffer(x, "x", bf16, (rows, k), dev), _buffer(w, "w", bf16, (experts, n, k), dev),
+            _buffer(bias, "bias", bf16, (experts, n), dev, optional=True),
+            _buffer(residual, "residual", bf16, (rows, n), dev, optional=True),
+            _offsets(expert_first_token_offset, experts, dev), experts, rows, n, k, act,
+            _buffer(pre_activation, "pre_activation", bf16, (rows, n), dev, optional=True),
+            _buffer(y, "y", bf16, (rows, n), dev))
+    _call("moe_grouped_linear_bf16", dev, stream, args)
 
 
 def moe_grouped_linear_backward_bf16(d_y, x, w, expert_first_token_offset, d_x=None, d_w=None, d_bias=None,
@@ -182,22 +187,18 @@ def moe_grouped_linear_backward_bf16(d_y, x, w, expert_first_token_offset, d_x=N
     act = _activation(activation)
     experts, n, k = _matrix(w, "w", 3).shape
     rows = _matrix(d_y, "d_y", 2).shape[0]
-    dev = d_y.device
-    if act == MOE_ACT_NONE and (pre_activation is not None or d_pre_activation is not None):
+    dev, bf16, plain = d_y.device, _bf16(), act == MOE_ACT_NONE
+    if plain and (pre_activation is not None or d_pre_activation is not None):
         raise ValueError("pre_activation and d_pre_activation go with an activation")
-    _shaped(d_y, "d_y", (rows, n), dev)
-    _shaped(x, "x", (rows, k), dev, optional=d_w is None)
-    _shaped(w, "w", (experts, n, k), dev)
-    _shaped(d_x, "d_x", (rows, k), dev, optional=True)
-    _shaped(d_w, "d_w", (experts, n, k), dev, optional=True)
-    _shaped(d_bias, "d_bias", (experts, n), dev, optional=True)
-    _shaped(pre_activation, "pre_activation", (rows, n), dev, optional=act == MOE_ACT_NONE)
-    _shaped(d_pre_activation, "d_pre_activation", (rows, n), dev, optional=act == MOE_ACT_NONE)
-    _offsets(expert_first_token_offset, experts, dev)
-    _require_gpu(dev)
-    _call("moe_grouped_linear_backward_bf16", dev, stream, d_y,
-          (_ptr(d_y), _ptr(pre_activation), _ptr(x), _ptr(w), _ptr(expert_first_token_offset), experts, rows, n, k,
-           act, _ptr(d_pre_activation), _ptr(d_x), _ptr(d_w), _ptr(d_bias)))
+    args = (_buffer(d_y, "d_y", bf16, (rows, n), dev),
+            _buffer(pre_activation, "pre_activation", bf16, (rows, n), dev, optional=plain),
+            _buffer(x, "x", bf16, (rows, k), dev, optional=d_w is None), _buffer(w, "w", bf16, (experts, n, k), dev),
+            _offsets(expert_first_token_offset, experts, dev), experts, rows, n, k, act,
+            _buffer(d_pre_activation, "d_pre_activation", bf16, (rows, n), dev, optional=plain),
+            _buffer(d_x, "d_x", bf16, (rows, k), dev, optional=True),
+            _buffer(d_w, "d_w", bf16, (experts, n, k), dev, optional=True),
+            _buffer(d_bias, "d_bias", bf16, (experts, n), dev, optional=True))
+    _call("moe_grouped_linear_backward_bf16", dev, stream, args)
 
 
 def moe_unpermute_backward(d_output, expanded_output, topk_weights, inv_permuted_idx, d_expanded_output=None,
@@ -216,14 +217,11 @@ def moe_unpermute_backward(d_output, expanded_output, topk_weights, inv_permuted
     dev = d_output.device
     if d_output.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("d_output must be float32 or bfloat16, got %s" % d_output.dtype)
-    same = (d_output.dtype,)
-    _check(d_output, "d_output", same, n * h, dev)
-    _check(expanded_output, "expanded_output", same, n * topk * h, dev, optional=d_topk_weights is None)
-    _check(topk_weights, "topk_weights", (torch.float32,), n * topk, dev)
-    _check(inv_permuted_idx, "inv_permuted_idx", (torch.int32,), n * topk, dev)
-    _check(d_expanded_output, "d_expanded_output", same, n * topk * h, dev, optional=True)
-    _check(d_topk_weights, "d_topk_weights", (torch.float32,), n * topk, dev, optional=True)
-    _require_gpu(dev)
-    _call("moe_unpermute_backward", dev, stream, d_output,
-          (_ptr(d_output), _ptr(expanded_output), _dtype_code(d_output), _ptr(topk_weights), _ptr(inv_permuted_idx),
-           n, h, topk, _ptr(d_expanded_output), _ptr(d_topk_weights)))
+    same, f32, slots = (d_output.dtype,), (torch.float32,), n * topk
+    args = (_buffer(d_output, "d_output", same, (n, h), dev),
+            _buffer(expanded_output, "expanded_output", same, (slots, h), dev, optional=d_topk_weights is None),
+            _dtype_code(d_output), _buffer(topk_weights, "topk_weights", f32, (n, topk), dev),
+            _buffer(inv_permuted_idx, "inv_permuted_idx", (torch.int32,), (slots,), dev), n, h, topk,
+            _buffer(d_expanded_output, "d_expanded_output", same, (slots, h), dev, optional=True),
+            _buffer(d_topk_weights, "d_topk_weights", f32, (n, topk), dev, optional=True))
+    _call("moe_unpermute_backward", dev, stream, args)
