@@ -85,25 +85,27 @@ __device__ __forceinline__ TileCoord tile_coord(int64_t id, const int64_t* pre, 
     return t;
 }
 
-// Calls f(row of the tile, column within the wave's 32-column block, values
-// even, values odd) for every pair of runs (columns 16 p + 4 (l / 32) .. and 8
-// further) of row block (h, fb): the column given is that of the pair's vector.
+// Calls f(h, f, first row) for each of the wave's 32-row blocks of the tile.
 template <typename F>
-__device__ __forceinline__ void for_each_pair(int wm, int lane, F&& f) {
+__device__ __forceinline__ void for_each_block(int wm, F&& f) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int fb = 0; fb < 2; ++fb)
-#pragma unroll
-            for (int p = 0; p < 2; ++p) f(h, fb, p, h * 128 + wm * 64 + fb * 32 + lane % 32, p * 16 + lane / 32 * 8);
+        for (int fb = 0; fb < 2; ++fb) f(h, fb, h * 128 + wm * 64 + fb * 32);
 }
 
-__device__ __forceinline__ u32x2 pack4(const f32x16& v, int j) {
-    return u32x2{pack_bf16(v[4 * j], v[4 * j + 1]), pack_bf16(v[4 * j + 2], v[4 * j + 3])};
+// A block's sums, rounded, into `dst` at (row, col).
+__device__ __forceinline__ void store_block(const WaveBlock& block, const TileMatrix& dst, int row, int col, int lane,
+                                            const f32x16& v) {
+    u32x2 runs[4];
+    u32x4 out[2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        runs[j] = u32x2{pack_bf16(v[4 * j], v[4 * j + 1]), pack_bf16(v[4 * j + 2], v[4 * j + 3])};
+    block.to_vectors(runs, out);
+    dst.store(row, col, lane, out);
 }
-__device__ __forceinline__ u32x4 pack_pair(const f32x16& v, int p) {
-    return runs_to_vector(pack4(v, 2 * p), pack4(v, 2 * p + 1));
-}
+
 __device__ __forceinline__ void add4(f32x16& v, int j, u32x2 w) {
     v[4 * j] += bf16_low(w[0]);
     v[4 * j + 1] += bf16_high(w[0]);
@@ -119,11 +121,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
     constexpr bool kBTc = kP == Product::kForward;     // w rows
     constexpr int kColsPerTile = kGated ? kTileCols / 2 : kTileCols;
     __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
-    __shared__ int64_t pre_s[kMaxExperts + 1], off_s[kMaxExperts + 1];
+    __shared__ __attribute__((aligned(1024))) char blocks[kTileThreads / 64 * kBlockBytes];
+    __shared__ int64_t pre_s[kMaxExperts + 1];
     __shared__ int64_t part[kTileThreads / 64];
     const int64_t cols = kP == Product::kForward ? p.n : p.k;
     const int64_t col_tiles = (cols + kColsPerTile - 1) / kColsPerTile;
-    for (int i = threadIdx.x; i <= p.num_experts; i += kTileThreads) off_s[i] = p.off[i];
     const bool ok = expert_items<kTileThreads>(p.off, p.num_experts, p.max_rows, pre_s, part, [&](int64_t rows) {
         const int64_t r = kWg ? p.m : rows;
         return (r + kTileRows - 1) / kTileRows * col_tiles;
@@ -180,7 +182,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
         return o;
     };
     auto coord_of = [&](int64_t id) __attribute__((always_inline)) {
-        return tile_coord<kWg>(id, pre_s, off_s, p.num_experts, p.m, col_tiles, kColsPerTile);
+        return tile_coord<kWg>(id, pre_s, p.off, p.num_experts, p.m, col_tiles, kColsPerTile);
     };
     // Stores of every tile at least (vectors of its outputs, per lane).
     constexpr int kStores = kGated ? 8 : 16;
@@ -208,21 +210,22 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
         const int64_t row0 = (kWg ? (int64_t)t.expert * p.m : t.first) + t.r0;
         const int rl = (int)(rows_left < kTileRows ? rows_left : kTileRows);
         const int cl = (int)(cols - t.c0 < kColsPerTile ? cols - t.c0 : kColsPerTile);
+        const WaveBlock block(blocks, wave, lane);
         if constexpr (kGated) {
             if (p.pre != nullptr) {
                 const TileMatrix gate(p.pre + row0 * p.m + t.c0, p.m, t.c0, rl, cl);
                 const TileMatrix up(p.pre + row0 * p.m + p.n + t.c0, p.m, p.n + t.c0, rl, cl);
-                for_each_pair(wm, lane, [&](int h, int f, int q, int r, int c) {
-                    gate.store(r, wn * 32 + c, pack_pair(sums.v[h][f][0], q));
-                    up.store(r, wn * 32 + c, pack_pair(sums.v[h][f][1], q));
+                for_each_block(wm, [&](int h, int f, int r) {
+                    store_block(block, gate, r, wn * 32, lane, sums.v[h][f][0]);
+                    store_block(block, up, r, wn * 32, lane, sums.v[h][f][1]);
                 });
             }
             const TileMatrix out(p.out + row0 * p.n + t.c0, p.n, t.c0, rl, cl);
-            for_each_pair(wm, lane, [&](int h, int f, int q, int r, int c) {
+            for_each_block(wm, [&](int h, int f, int r) {
                 f32x16& v = sums.v[h][f][0];
 #pragma unroll
-                for (int i = 8 * q; i < 8 * q + 8; ++i) v[i] = act_value<kAct>(v[i]) * sums.v[h][f][1][i];
-                out.store(r, wn * 32 + c, pack_pair(v, q));
+                for (int i = 0; i < 16; ++i) v[i] = act_value<kAct>(v[i]) * sums.v[h][f][1][i];
+                store_block(block, out, r, wn * 32, lane, v);
             });
         } else {
             const TileMatrix out(p.out + row0 * cols + t.c0, cols, t.c0, rl, cl);
@@ -244,25 +247,27 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
                                 for (int f = 0; f < 2; ++f) add4(sums.v[h][f][cb], j, bv);
                         }
                     }
-                    for_each_pair(wm, lane, [&](int h, int f, int q, int r, int c) {
+                    for_each_block(wm, [&](int h, int f, int r) {
                         f32x16& v = sums.v[h][f][cb];
-                        if (p.pre != nullptr) pre.store(r, col + c, pack_pair(v, q));
+                        if (p.pre != nullptr) store_block(block, pre, r, col, lane, v);
 #pragma unroll
-                        for (int i = 8 * q; i < 8 * q + 8; ++i) v[i] = act_value<kAct>(v[i]);
+                        for (int i = 0; i < 16; ++i) v[i] = act_value<kAct>(v[i]);
                         if (p.residual != nullptr) {
-                            u32x2 even, odd;
-                            vector_to_runs(res.load(r, col + c), even, odd);
-                            add4(v, 2 * q, even);
-                            add4(v, 2 * q + 1, odd);
+                            u32x4 rv[2];
+                            u32x2 runs[4];
+                            res.load(r, col, lane, rv);
+                            block.to_runs(rv, runs);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) add4(v, j, runs[j]);
                         }
-                        out.store(r, col + c, pack_pair(v, q));
+                        store_block(block, out, r, col, lane, v);
                     });
                 }
             } else {
 #pragma unroll
                 for (int cb = 0; cb < 2; ++cb)
-                    for_each_pair(wm, lane, [&](int h, int f, int q, int r, int c) {
-                        out.store(r, wn * 64 + cb * 32 + c, pack_pair(sums.v[h][f][cb], q));
+                    for_each_block(wm, [&](int h, int f, int r) {
+                        store_block(block, out, r, wn * 64 + cb * 32, lane, sums.v[h][f][cb]);
                     });
             }
         }

@@ -374,29 +374,56 @@ __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool
     phase_barrier();
 }
 
-// Two of a lane's runs of four consecutive outputs, 8 columns apart (columns
-// 16 p + 4 (l / 32) .. and 16 p + 8 + 4 (l / 32) ..), and one 16-byte vector of
-// eight consecutive columns, 16 p + 8 (l / 32) ..: the halves of the wave
-// exchange a run each.  v_permlane32_swap_b32 swaps the upper half of its
-// first register with the lower half of its second; it is its own inverse.
-__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-}
-__device__ __forceinline__ u32x4 runs_to_vector(u32x2 even, u32x2 odd) {
-    uint32_t e0 = even[0], e1 = even[1], o0 = odd[0], o1 = odd[1];
-    swap_halves(e0, o0);
-    swap_halves(e1, o1);
-    return u32x4{e0, e1, o0, o1};
-}
-__device__ __forceinline__ void vector_to_runs(u32x4 v, u32x2& even, u32x2& odd) {
-    uint32_t e0 = v[0], e1 = v[1], o0 = v[2], o1 = v[3];
-    swap_halves(e0, o0);
-    swap_halves(e1, o1);
-    even = u32x2{e0, e1};
-    odd = u32x2{o0, o1};
-}
+// Between the sums' layout and rows of memory.  A wave's 32 x 32 block of
+// results, a lane's four runs of four consecutive columns (columns 8 j +
+// 4 (l / 32) .. of row l % 32, j = 0 .. 3) against two 16-byte vectors (row
+// 16 i + l / 4, columns 8 (l % 4) .., i = 0, 1), through 2 KiB of LDS of the
+// wave's own.  Stored as they are, the runs would write 16 bytes of each of 32
+// rows an instruction, exchanged between the halves of the wave 32 bytes (62
+// cycles an instruction, 8000 of a tile); runs of 64 bytes take 35.
+// A wave's LDS operations execute in order, so the write and the read back need
+// no wait between them; as in the k-loop the statement waits for its own reads.
+// Rows of 64 bytes, 16-byte slot v of row r at v ^ (r / 4) % 4.
+constexpr int kBlockBytes = 32 * 64;
+
+struct WaveBlock {
+    uint32_t run;     // LDS address of this lane's run 0; run j: with j * 16 flipped
+    uint32_t vector;  // of its vector 0; vector 1 lies 1 KiB on
+
+    __device__ __forceinline__ WaveBlock(const char* lds, int wave, int lane) {
+        const uint32_t base = (uint32_t)(uintptr_t)lds + wave * kBlockBytes;
+        const int r = lane % 32;
+        run = base + r * 64 + ((r / 4) % 4) * 16 + lane / 32 * 8;
+        vector = base + lane / 4 * 64 + ((lane % 4) ^ (lane / 16)) * 16;
+    }
+    __device__ __forceinline__ void to_vectors(const u32x2 (&runs)[4], u32x4 (&v)[2]) const {
+        asm volatile(
+            "ds_write_b64 %2, %6\n\t"
+            "ds_write_b64 %3, %7\n\t"
+            "ds_write_b64 %4, %8\n\t"
+            "ds_write_b64 %5, %9\n\t"
+            "ds_read_b128 %0, %10\n\t"
+            "ds_read_b128 %1, %10 offset:1024\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0]), "=&v"(v[1])
+            : "v"(run), "v"(run ^ 16u), "v"(run ^ 32u), "v"(run ^ 48u), "v"(runs[0]), "v"(runs[1]), "v"(runs[2]),
+              "v"(runs[3]), "v"(vector)
+            : "memory");
+    }
+    __device__ __forceinline__ void to_runs(const u32x4 (&v)[2], u32x2 (&runs)[4]) const {
+        asm volatile(
+            "ds_write_b128 %8, %9\n\t"
+            "ds_write_b128 %8, %10 offset:1024\n\t"
+            "ds_read_b64 %0, %4\n\t"
+            "ds_read_b64 %1, %5\n\t"
+            "ds_read_b64 %2, %6\n\t"
+            "ds_read_b64 %3, %7\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(runs[0]), "=&v"(runs[1]), "=&v"(runs[2]), "=&v"(runs[3])
+            : "v"(run), "v"(run ^ 16u), "v"(run ^ 32u), "v"(run ^ 48u), "v"(vector), "v"(v[0]), "v"(v[1])
+            : "memory");
+    }
+};
 
 // A tile's rows and columns in a row-major bf16 matrix, as a buffer resource:
 // vectors past its rows or columns are not stored and read as zero, so every
@@ -417,11 +444,18 @@ struct TileMatrix {
     __device__ __forceinline__ int offset(int row, int col) const {
         return (int)(col < cols ? (uint32_t)row * row_bytes + (uint32_t)col * 2 : kOutOfRange);
     }
-    __device__ __forceinline__ void store(int row, int col, u32x4 v) const {
-        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, offset(row, col), 0, 0);
+    // The two vectors of the 32 x 32 block at (row, col) that WaveBlock gives this lane.
+    __device__ __forceinline__ void store(int row, int col, int lane, const u32x4 (&v)[2]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            __builtin_amdgcn_raw_buffer_store_b128(v[i], rsrc, offset(row + i * 16 + lane / 4, col + lane % 4 * 8), 0,
+                                                   0);
     }
-    __device__ __forceinline__ u32x4 load(int row, int col) const {
-        return __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset(row, col), 0, 0);
+    __device__ __forceinline__ void load(int row, int col, int lane, u32x4 (&v)[2]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            v[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset(row + i * 16 + lane / 4, col + lane % 4 * 8), 0,
+                                                         0);
     }
 };
 
