@@ -31,6 +31,10 @@ enum class Product { kForward, kInputGrad, kWeightGrad, kWeightBiasGrad };
 constexpr int kXcdCount = 8;
 constexpr int64_t kGroupRows = 8;  // row tiles per group in the tile order
 
+// Cost of a tile outside its k-loop, and of a small tile's step, in steps of a
+// large one (1.5 us with every CU busy; 10 us and 0.6 - 0.7 us measured).
+constexpr double kFixedCost = 6.0, kSmallStepCost = 0.45, kSmallFixedCost = 3.0;
+
 struct GemmParams {
     const int64_t* off;
     int num_experts;
@@ -65,7 +69,7 @@ struct TileCoord {
 // Order of an expert's tiles: groups of kGroupRows row tiles, within a group
 // row tiles fastest, then column tiles; a remainder of up to three row tiles
 // joins the last group (it would stream every column tile again for itself).
-template <bool kWeightGrad>
+template <bool kWeightGrad, int kRows>
 __device__ __forceinline__ TileCoord tile_coord(int64_t id, const int64_t* pre, const int64_t* off, int num_experts,
                                                 int64_t m, int64_t col_tiles, int cols_per_tile) {
     TileCoord t;
@@ -73,25 +77,25 @@ __device__ __forceinline__ TileCoord tile_coord(int64_t id, const int64_t* pre, 
     t.first = wave_uniform64(off[t.expert]);
     t.count = wave_uniform64(off[t.expert + 1]) - t.first;
     const int64_t local = id - wave_uniform64(pre[t.expert]);
-    const int64_t mt = ((kWeightGrad ? m : t.count) + kTileRows - 1) / kTileRows;
+    const int64_t mt = ((kWeightGrad ? m : t.count) + kRows - 1) / kRows;
     const int64_t left = mt % kGroupRows;
     const int64_t groups = mt / kGroupRows + (left > 3 || mt < kGroupRows);
     int64_t rem;
     const int64_t g0 = divide(local, kGroupRows * col_tiles, rem), g = g0 < groups - 1 ? g0 : groups - 1;
     const int64_t gsize = g == groups - 1 ? mt - g * kGroupRows : kGroupRows;
     const int64_t ct = divide(local - g * kGroupRows * col_tiles, gsize, rem);
-    t.r0 = wave_uniform64((g * kGroupRows + rem) * kTileRows);
+    t.r0 = wave_uniform64((g * kGroupRows + rem) * kRows);
     t.c0 = wave_uniform64(ct * cols_per_tile);
     return t;
 }
 
 // Calls f(h, f, first row) for each of the wave's 32-row blocks of the tile.
-template <typename F>
+template <typename S, typename F>
 __device__ __forceinline__ void for_each_block(int wm, F&& f) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < S::kHalves; ++h)
 #pragma unroll
-        for (int fb = 0; fb < 2; ++fb) f(h, fb, h * 128 + wm * 64 + fb * 32);
+        for (int fb = 0; fb < S::kBlocks; ++fb) f(h, fb, h * 128 + wm * 32 * S::kBlocks + fb * 32);
 }
 
 // A block's sums, rounded, into `dst` at (row, col).
@@ -113,13 +117,14 @@ __device__ __forceinline__ void add4(f32x16& v, int j, u32x2 w) {
     v[4 * j + 3] += bf16_high(w[1]);
 }
 
-template <Product kP, bool kGated, int kAct>
+template <Product kP, bool kGated, int kAct, bool kSmall>
 __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmParams p) {
+    typedef TileShape<kSmall> S;
     constexpr bool kBiasGrad = kP == Product::kWeightBiasGrad;
     constexpr bool kWg = kP == Product::kWeightGrad || kBiasGrad;
     constexpr bool kATc = !kWg;                        // x, d_z rows: T-contiguous
     constexpr bool kBTc = kP == Product::kForward;     // w rows
-    constexpr int kColsPerTile = kGated ? kTileCols / 2 : kTileCols;
+    constexpr int kColsPerTile = kGated ? S::kCols / 2 : S::kCols;
     __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
     __shared__ __attribute__((aligned(1024))) char blocks[kTileThreads / 64 * kBlockBytes];
     __shared__ int64_t pre_s[kMaxExperts + 1];
@@ -128,12 +133,12 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
     const int64_t col_tiles = (cols + kColsPerTile - 1) / kColsPerTile;
     const bool ok = expert_items<kTileThreads>(p.off, p.num_experts, p.max_rows, pre_s, part, [&](int64_t rows) {
         const int64_t r = kWg ? p.m : rows;
-        return (r + kTileRows - 1) / kTileRows * col_tiles;
+        return (r + S::kRows - 1) / S::kRows * col_tiles;
     });
     if (!ok) return;
     const int64_t total = wave_uniform64(pre_s[p.num_experts]);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int wm = wave / 4, wn = wave % 4;
+    const int wm = wave / S::kWavesAcross, wn = wave % S::kWavesAcross;
     // Workgroups are dispatched round-robin over the XCDs; the tiles running at
     // once are split into one contiguous chunk per XCD, so that an XCD's L2
     // serves neighbouring tiles.
@@ -143,7 +148,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
     auto operands_of = [&](const TileCoord& t) __attribute__((always_inline)) {
         TileOperands o{};
         const int64_t rows_left = (kWg ? p.m : t.count) - t.r0, cols_left = cols - t.c0;
-        const int64_t extent_a = rows_left < kTileRows ? rows_left : kTileRows;
+        const int64_t extent_a = rows_left < S::kRows ? rows_left : S::kRows;
         const int64_t extent_b = cols_left < kColsPerTile ? cols_left : kColsPerTile;
         o.a_row = o.b_row = wave * 16;
         if constexpr (kP == Product::kForward) {
@@ -182,46 +187,45 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
         return o;
     };
     auto coord_of = [&](int64_t id) __attribute__((always_inline)) {
-        return tile_coord<kWg>(id, pre_s, p.off, p.num_experts, p.m, col_tiles, kColsPerTile);
+        return tile_coord<kWg, S::kRows>(id, pre_s, p.off, p.num_experts, p.m, col_tiles, kColsPerTile);
     };
     // Stores of every tile at least (vectors of its outputs, per lane).
-    constexpr int kStores = kGated ? 8 : 16;
+    constexpr int kStores = S::kHalves * S::kBlocks * (kGated ? 2 : 4);
 
     if (slot >= total) return;
     TileCoord next = coord_of(slot);
     TileOperands ops = operands_of(next);
-    begin_tile<kATc, kBTc>(lds, ops);
+    begin_tile<kSmall, kATc, kBTc>(lds, ops);
     for (int64_t id = slot; id < total; id += grid) {
         const TileCoord t = next;
         const bool more = id + grid < total;
         const int64_t rows_left = (kWg ? p.m : t.count) - t.r0;
-        TileSums sums;
-        clear_sums(sums);
+        TileSums<kSmall> sums;
         if (more) next = coord_of(id + grid);  // while the first loads are under way
         tile_sums<kATc, kBTc, kStores, kBiasGrad>(lds, ops, id == slot, rows_left > 128, sums);
         // The next tile's first loads go out ahead of this tile's stores and
         // land while the results are worked out.
         if (more) {
             ops = operands_of(next);
-            begin_tile<kATc, kBTc>(lds, ops);
+            begin_tile<kSmall, kATc, kBTc>(lds, ops);
         }
 
         const int lane = opaque_lane();
         const int64_t row0 = (kWg ? (int64_t)t.expert * p.m : t.first) + t.r0;
-        const int rl = (int)(rows_left < kTileRows ? rows_left : kTileRows);
+        const int rl = (int)(rows_left < S::kRows ? rows_left : S::kRows);
         const int cl = (int)(cols - t.c0 < kColsPerTile ? cols - t.c0 : kColsPerTile);
         const WaveBlock block(blocks, wave, lane);
         if constexpr (kGated) {
             if (p.pre != nullptr) {
                 const TileMatrix gate(p.pre + row0 * p.m + t.c0, p.m, t.c0, rl, cl);
                 const TileMatrix up(p.pre + row0 * p.m + p.n + t.c0, p.m, p.n + t.c0, rl, cl);
-                for_each_block(wm, [&](int h, int f, int r) {
+                for_each_block<S>(wm, [&](int h, int f, int r) {
                     store_block(block, gate, r, wn * 32, lane, sums.v[h][f][0]);
                     store_block(block, up, r, wn * 32, lane, sums.v[h][f][1]);
                 });
             }
             const TileMatrix out(p.out + row0 * p.n + t.c0, p.n, t.c0, rl, cl);
-            for_each_block(wm, [&](int h, int f, int r) {
+            for_each_block<S>(wm, [&](int h, int f, int r) {
                 f32x16& v = sums.v[h][f][0];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = act_value<kAct>(v[i]) * sums.v[h][f][1][i];
@@ -242,12 +246,12 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
                             u32x2 bv = {0u, 0u};
                             if (c < cl) bv = *reinterpret_cast<const u32x2*>(p.bias + t.expert * p.n + t.c0 + c);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
+                            for (int h = 0; h < S::kHalves; ++h)
 #pragma unroll
-                                for (int f = 0; f < 2; ++f) add4(sums.v[h][f][cb], j, bv);
+                                for (int f = 0; f < S::kBlocks; ++f) add4(sums.v[h][f][cb], j, bv);
                         }
                     }
-                    for_each_block(wm, [&](int h, int f, int r) {
+                    for_each_block<S>(wm, [&](int h, int f, int r) {
                         f32x16& v = sums.v[h][f][cb];
                         if (p.pre != nullptr) store_block(block, pre, r, col, lane, v);
 #pragma unroll
@@ -266,7 +270,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
             } else {
 #pragma unroll
                 for (int cb = 0; cb < 2; ++cb)
-                    for_each_block(wm, [&](int h, int f, int r) {
+                    for_each_block<S>(wm, [&](int h, int f, int r) {
                         store_block(block, out, r, wn * 64 + cb * 32, lane, sums.v[h][f][cb]);
                     });
             }
@@ -276,11 +280,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
             // tile's first waves hold them, half of T in lanes l and l + 32.
             if (t.c0 == 0 && wn == 0) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < S::kHalves; ++h)
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
+                    for (int f = 0; f < S::kBlocks; ++f) {
                         const float lo = sums.a_sum[h][f], sum = lo + __shfl_xor(lo, 32, 64);
-                        const int r = h * 128 + wm * 64 + f * 32 + lane;
+                        const int r = h * 128 + wm * 32 * S::kBlocks + f * 32 + lane;
                         if (lane < 32 && r < rl) p.d_bias[row0 + r] = (uint16_t)pack_bf16(sum, 0.0f);
                     }
             }
@@ -289,13 +293,32 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
     }
 }
 
+// Whether a product runs faster on small tiles: its rounds of workgroups times
+// what a tile takes.  rows: output rows of all experts; groups: experts that may
+// have rows (each ends in half a tile on average).  Small / large tiles, us:
+// one expert 1024^3 18.1 / 27.9, 2048^3 29 / 54, 4096 x 4096 x 512 37.7 / 26.1;
+// 8 experts of 300 rows, 1024 x 1024 18 / 29.5, of 1024, 2048 x 2048 125 / 104;
+// 128 of 64, 768 x 2048 112 / 127, of 128 144 / 134.
+bool small_tiles(int64_t rows, int64_t groups, int64_t cols, int64_t cols_large, int64_t depth, int num_cus) {
+    auto cost = [&](int64_t tile, int64_t tile_cols, double step, double fixed) {
+        const int64_t row_tiles = (rows + tile - 1) / tile + (groups > 1 ? (groups - 1) / 2 : 0);
+        const int64_t tiles = row_tiles * ((cols + tile_cols - 1) / tile_cols);
+        const int64_t rounds = (tiles + num_cus - 1) / num_cus;
+        return (double)rounds * ((double)((depth + kStepT - 1) / kStepT) * step + fixed);
+    };
+    return cost(128, cols_large / 2, kSmallStepCost, kSmallFixedCost) < cost(256, cols_large, 1.0, kFixedCost);
+}
+
 template <Product kP, bool kGated, int kAct>
-hipError_t launch_product(const GemmParams& p, int num_cus, hipStream_t stream) {
+hipError_t launch_product(const GemmParams& p, bool small, int num_cus, hipStream_t stream) {
     const int blocks = num_cus < kXcdCount ? kXcdCount : num_cus / kXcdCount * kXcdCount;
-    hipLaunchKernelGGL((expert_product_kernel<kP, kGated, kAct>), dim3((unsigned)blocks), dim3(kTileThreads), 0,
-                       stream, p);
+    auto* kernel = small ? expert_product_kernel<kP, kGated, kAct, true> : expert_product_kernel<kP, kGated, kAct, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kTileThreads), 0, stream, p);
     return hipGetLastError();
 }
+
+// Experts that may have rows.
+int64_t most_groups(const ExpertRows& r) { return r.max_rows < r.num_experts ? r.max_rows : r.num_experts; }
 
 GemmParams params_of(const ExpertRows& rows, int64_t m, int64_t k, const void* a, const void* b, void* out) {
     GemmParams p{};
@@ -320,23 +343,28 @@ hipError_t launch_expert_forward(const ExpertForwardArgs& a, int num_cus, hipStr
     p.bias = static_cast<const uint16_t*>(a.bias);
     p.residual = static_cast<const uint16_t*>(a.residual);
     p.pre = static_cast<uint16_t*>(a.pre);
+    const bool small = small_tiles(a.rows.max_rows, most_groups(a.rows), a.n, a.gated ? 128 : 256, a.k, num_cus);
     return with_activation(a.activation, [&](auto act) {
         constexpr int kAct = decltype(act)::value;
-        return a.gated ? launch_product<Product::kForward, true, kAct>(p, num_cus, stream)
-                       : launch_product<Product::kForward, false, kAct>(p, num_cus, stream);
+        return a.gated ? launch_product<Product::kForward, true, kAct>(p, small, num_cus, stream)
+                       : launch_product<Product::kForward, false, kAct>(p, small, num_cus, stream);
     });
 }
 
 hipError_t launch_expert_input_grad(const ExpertInputGradArgs& a, int num_cus, hipStream_t stream) {
-    return launch_product<Product::kInputGrad, false, kActNone>(params_of(a.rows, a.m, a.k, a.d_z, a.w, a.d_x),
+    const bool small = small_tiles(a.rows.max_rows, most_groups(a.rows), a.k, 256, a.m, num_cus);
+    return launch_product<Product::kInputGrad, false, kActNone>(params_of(a.rows, a.m, a.k, a.d_z, a.w, a.d_x), small,
                                                                 num_cus, stream);
 }
 
 hipError_t launch_expert_weight_grad(const ExpertWeightGradArgs& a, int num_cus, hipStream_t stream) {
     GemmParams p = params_of(a.rows, a.m, a.k, a.d_z, a.x, a.d_w);
     p.d_bias = static_cast<uint16_t*>(a.d_bias);
-    return p.d_bias != nullptr ? launch_product<Product::kWeightBiasGrad, false, kActNone>(p, num_cus, stream)
-                               : launch_product<Product::kWeightGrad, false, kActNone>(p, num_cus, stream);
+    // every expert has all its tiles; T is its share of the rows
+    const int64_t e = a.rows.num_experts;
+    const bool small = small_tiles(a.m * e, 0, a.k, 256, a.rows.max_rows / e + 1, num_cus);
+    return p.d_bias != nullptr ? launch_product<Product::kWeightBiasGrad, false, kActNone>(p, small, num_cus, stream)
+                               : launch_product<Product::kWeightGrad, false, kActNone>(p, small, num_cus, stream);
 }
 
 }  // namespace moe

@@ -35,11 +35,24 @@ namespace moe {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kTileRows = 256, kTileCols = 256, kStepT = 64;
+constexpr int kStepT = 64;
 constexpr int kTileThreads = 512;
 constexpr int kHalfBytes = 128 * kStepT * 2;       // one half tile
 constexpr int kStageBytes = 4 * kHalfBytes;        // A0, A1, B0, B1
 constexpr int kTileLds = 2 * kStageBytes;
+
+// Tiles of 256 x 256 and, for products with too few of those to fill the GPU,
+// of 128 x 128 (kSmall): there 4 x 2 waves of 32 x 64, and the LDS a ring of
+// four stages of one half tile of each operand.
+template <bool kSmall>
+struct TileShape {
+    static constexpr int kRows = kSmall ? 128 : 256, kCols = kSmall ? 128 : 256;
+    static constexpr int kHalves = kSmall ? 1 : 2;     // halves of 128 rows
+    static constexpr int kBlocks = kSmall ? 1 : 2;     // 32-row blocks of a wave in a half
+    static constexpr int kWavesAcross = kSmall ? 2 : 4;
+};
+constexpr int kSmallStageBytes = 2 * kHalfBytes, kSmallStages = 4;
+static_assert(kSmallStages * kSmallStageBytes == kTileLds, "both shapes use the same LDS");
 constexpr int kPartA = 0, kPartB = 2;              // first half tile of each operand in a stage
 constexpr uint32_t kOutOfRange = 0x80000000u;      // a byte offset past every resource (all hold less than 2^31 bytes)
 
@@ -137,16 +150,16 @@ __device__ __forceinline__ void load_half(char* dst, __amdgpu_buffer_rsrc_t rsrc
     }
 }
 
-// Byte offset of this lane's first fragment vector in a half tile, for the
-// 64-row block `block` (0 or 1) of the half.
+// Byte offset of this lane's first fragment vector in a half tile, for the rows
+// from `row` (a multiple of 64, or of 32 for a single block).
 template <bool kTContig>
-__device__ __forceinline__ uint32_t frag_offset(int block, int lane) {
+__device__ __forceinline__ uint32_t frag_offset(int row, int lane) {
     if constexpr (kTContig) {
-        const int r = block * 64 + lane % 32;
+        const int r = row + lane % 32;
         return (uint32_t)(r * 128 + t_slot(r, lane / 32) * 16);
     } else {
         const int g = lane / 16, i = lane % 16;
-        const int t = (g / 2) * 8 + i / 4, unit = block * 4 + g % 2;
+        const int t = (g / 2) * 8 + i / 4, unit = row / 16 + g % 2;
         return (uint32_t)(t * 256 + (unit ^ (2 * (i / 4))) * 32 + (i % 4) * 8);
     }
 }
@@ -219,38 +232,85 @@ __device__ __forceinline__ void read_frags(uint32_t a, Frags& fr) {
     else read_r_contig(a, fr);
 }
 
+// The four fragments of one 32-row block.
+template <bool kTContig>
+__device__ __forceinline__ void read_block(uint32_t a, bf16x8 (&fr)[4]) {
+    if constexpr (kTContig) {
+        u32x4 r[4];
+        asm volatile(
+            "ds_read_b128 %0, %4\n\t"
+            "ds_read_b128 %1, %5\n\t"
+            "ds_read_b128 %2, %6\n\t"
+            "ds_read_b128 %3, %7\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
+            : "v"(a), "v"(a ^ 32u), "v"(a ^ 64u), "v"(a ^ 96u)
+            : "memory");
+#pragma unroll
+        for (int s = 0; s < 4; ++s) fr[s] = __builtin_bit_cast(bf16x8, r[s]);
+    } else {
+        u32x2 r[8];
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %8\n\t"
+            "ds_read_b64_tr_b16 %1, %8 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %2, %8 offset:4096\n\t"
+            "ds_read_b64_tr_b16 %3, %8 offset:5120\n\t"
+            "ds_read_b64_tr_b16 %4, %8 offset:8192\n\t"
+            "ds_read_b64_tr_b16 %5, %8 offset:9216\n\t"
+            "ds_read_b64_tr_b16 %6, %8 offset:12288\n\t"
+            "ds_read_b64_tr_b16 %7, %8 offset:13312\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
+            : "v"(a)
+            : "memory");
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            fr[s] = __builtin_bit_cast(bf16x8, u32x4{r[2 * s][0], r[2 * s][1], r[2 * s + 1][0], r[2 * s + 1][1]});
+    }
+}
+
 // The tile's sums: half h, row block f, column block c of this wave.  Lane l,
 // register 4 j + q holds row 128 h + 64 wm + 32 f + l % 32, column
-// 64 wn + 32 c + 8 j + 4 (l / 32) + q (the MFMA takes the column operand first).
+// 64 wn + 32 c + 8 j + 4 (l / 32) + q (the MFMA takes the column operand first);
+// a small tile has h = f = 0, row 32 wm + l % 32.
 // a_sum: with kSumA, row 128 h + 64 wm + 32 f + l % 32 of operand a summed over
 // the T that lane l's fragments hold (the other half of them is in lane l ^ 32).
+template <bool kSmall>
 struct TileSums {
-    f32x16 v[2][2][2];
-    float a_sum[2][2];
+    typedef TileShape<kSmall> S;
+    f32x16 v[S::kHalves][S::kBlocks][2];
+    float a_sum[S::kHalves][S::kBlocks];
 };
 
-template <bool kSumA>
-__device__ __forceinline__ void multiply(const Frags& a, const Frags& b, f32x16 (&acc)[2][2], float (&a_sum)[2]) {
+// v plus the sum of a fragment's eight bf16 (dot products with ones: they run on
+// the vector units while the matrix cores work).
+__device__ __forceinline__ float sum8(bf16x8 frag, float v) {
+    const u32x4 w = __builtin_bit_cast(u32x4, frag);
+    const uint32_t ones = 0x3F803F80u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t wq = w[q];
+        v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, wq), __builtin_bit_cast(bf16x2, ones), v, false);
+    }
+    return v;
+}
+
+// acc += a b over a step, or = with kFirst (no registers to clear before).
+template <bool kSumA, bool kFirst, int kBlocks>
+__device__ __forceinline__ void multiply(const bf16x8 (&a)[kBlocks][4], const Frags& b, f32x16 (&acc)[kBlocks][2],
+                                         float (&a_sum)[kBlocks]) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+        for (int f = 0; f < kBlocks; ++f)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-                acc[f][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[c][s], a.v[f][s], acc[f][c], 0, 0, 0);
-        if constexpr (kSumA) {  // on the vector units, while the matrix cores work
-            const uint32_t ones = 0x3F803F80u;
+                acc[f][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    b.v[c][s], a[f][s], kFirst && s == 0 ? f32x16{} : acc[f][c], 0, 0, 0);
+        if constexpr (kSumA) {
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const u32x4 w = __builtin_bit_cast(u32x4, a.v[f][s]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t wq = w[q];
-                    a_sum[f] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, wq),
-                                                               __builtin_bit_cast(bf16x2, ones), a_sum[f], false);
-                }
-            }
+            for (int f = 0; f < kBlocks; ++f) a_sum[f] = sum8(a[f][s], kFirst && s == 0 ? 0.0f : a_sum[f]);
         }
     }
     __builtin_amdgcn_s_setprio(0);
@@ -290,6 +350,14 @@ struct TileLoader {
         const __amdgpu_buffer_rsrc_t ra = step_resource<kATc>(o.a, step, rem);
         load_half<kATc>(stage + kPartA * kHalfBytes, ra, a_voff, 0, rem, wave, lane);
     }
+    __device__ __forceinline__ void small(int64_t step) const {
+        char* stage = lds + (step % kSmallStages) * kSmallStageBytes;
+        int rem;
+        const __amdgpu_buffer_rsrc_t rb = step_resource<kBTc>(o.b, step, rem);
+        load_half<kBTc>(stage + kHalfBytes, rb, b_voff, 0, rem, wave, lane);
+        const __amdgpu_buffer_rsrc_t ra = step_resource<kATc>(o.a, step, rem);
+        load_half<kATc>(stage, ra, a_voff, 0, rem, wave, lane);
+    }
     __device__ __forceinline__ void a1(int64_t step) const {
         int rem;
         const __amdgpu_buffer_rsrc_t ra = step_resource<kATc>(o.a, step, rem);
@@ -299,26 +367,32 @@ struct TileLoader {
 };
 
 // The first loads of a tile: B and A0 of step 0 (6), A1 of step 0 (2), B and A0
-// of step 1 (6).  Every wave must be done with LDS.
-template <bool kATc, bool kBTc>
+// of step 1 (6); of a small tile steps 0 to 2 (4 each).  Every wave must be
+// done with LDS.
+template <bool kSmall, bool kATc, bool kBTc>
 __device__ __forceinline__ void begin_tile(char* lds, const TileOperands& o) {
     const TileLoader<kATc, kBTc> load(lds, o);
-    load.b_a0(0);
-    load.a1(0);
-    load.b_a0(1);
+    if constexpr (kSmall) {
+#pragma unroll
+        for (int s = 0; s < kSmallStages - 1; ++s) load.small(s);
+    } else {
+        load.b_a0(0);
+        load.a1(0);
+        load.b_a0(1);
+    }
     __builtin_amdgcn_sched_barrier(0);
 }
 
-__device__ __forceinline__ void clear_sums(TileSums& sums) {
+template <bool kSmall>
+__device__ __forceinline__ void clear_sums(TileSums<kSmall>& sums) {
+    typedef TileShape<kSmall> S;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < S::kHalves; ++h)
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                sums.v[h][f][c] = f32x16{};
-                sums.a_sum[h][f] = 0.0f;
-            }
+        for (int f = 0; f < S::kBlocks; ++f) {
+            sums.v[h][f][0] = sums.v[h][f][1] = f32x16{};
+            sums.a_sum[h][f] = 0.0f;
+        }
 }
 
 // The k-loop of a tile whose first loads are under way (begin_tile).  kStores:
@@ -329,13 +403,13 @@ __device__ __forceinline__ void clear_sums(TileSums& sums) {
 // no load is in flight and every wave is done with LDS.
 template <bool kATc, bool kBTc, int kStores, bool kSumA>
 __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool fresh, bool second_half,
-                                          TileSums& sums) {
+                                          TileSums<false>& sums) {
     static_assert(8 + kStores < 64, "vector-memory counter range");
     const TileLoader<kATc, kBTc> load(lds, o);
     const int lane = load.lane, wm = load.wave / 4, wn = load.wave % 4;
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-    const uint32_t a_frag = lds0 + kPartA * kHalfBytes + frag_offset<kATc>(wm, lane);
-    const uint32_t b_frag = lds0 + (kPartB + wn / 2) * kHalfBytes + frag_offset<kBTc>(wn % 2, lane);
+    const uint32_t a_frag = lds0 + kPartA * kHalfBytes + frag_offset<kATc>(wm * 64, lane);
+    const uint32_t b_frag = lds0 + (kPartB + wn / 2) * kHalfBytes + frag_offset<kBTc>(wn % 2 * 64, lane);
     const int64_t steps = (o.a.depth + kStepT - 1) / kStepT;
 
     __builtin_amdgcn_sched_barrier(0);
@@ -346,8 +420,9 @@ __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool
 
     auto run = [&](auto tag) __attribute__((always_inline)) {
         constexpr bool kBoth = decltype(tag)::value != 0;
-        auto one_step = [&](int64_t step, auto extra) __attribute__((always_inline)) {
-            constexpr int kExtra = decltype(extra)::value;
+        auto one_step = [&](int64_t step, auto first) __attribute__((always_inline)) {
+            constexpr bool kFirst = decltype(first)::value != 0;
+            constexpr int kExtra = kFirst ? kStores : 0;
             Frags fa, fb;
             const uint32_t stage = (uint32_t)(step % 2) * kStageBytes;
             load.a1(step + 1);
@@ -355,21 +430,62 @@ __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool
             read_frags<kATc>(a_frag + stage, fa);
             wait_loads<8 + kExtra>();  // A1 of this step; B, A0 (6) and A1 (2) of the next stay in flight
             phase_barrier();
-            multiply<kSumA>(fa, fb, sums.v[0], sums.a_sum[0]);
+            multiply<kSumA, kFirst, 2>(fa.v, fb, sums.v[0], sums.a_sum[0]);
             phase_barrier();
             load.b_a0(step + 2);       // into this stage: every wave has read its B and A0
             if constexpr (kBoth) read_frags<kATc>(a_frag + stage + kHalfBytes, fa);
             wait_loads<8 + kExtra>();  // B, A0 of the next step; its A1 (2) and the B, A0 after (6) stay in flight
             phase_barrier();
-            if constexpr (kBoth) multiply<kSumA>(fa, fb, sums.v[1], sums.a_sum[1]);
+            if constexpr (kBoth) multiply<kSumA, kFirst, 2>(fa.v, fb, sums.v[1], sums.a_sum[1]);
             phase_barrier();
         };
-        if (steps > 0) one_step(0, ActTag<kStores>{});
+        one_step(0, ActTag<1>{});
         for (int64_t step = 1; step < steps; ++step) one_step(step, ActTag<0>{});
     };
-    if (second_half) run(ActTag<1>{});
+    if (steps == 0) clear_sums(sums);  // no rows to sum over
+    else if (second_half) run(ActTag<1>{});
     else run(ActTag<0>{});
     if (wm == 0) phase_barrier();
+    wait_loads<0>();
+    phase_barrier();
+}
+
+// The same for a small tile: one phase a step (8 MFMAs a wave on 12 KiB of
+// fragments), three steps of loads ahead.
+template <bool kATc, bool kBTc, int kStores, bool kSumA>
+__device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool fresh, bool, TileSums<true>& sums) {
+    static_assert(8 + kStores < 64, "vector-memory counter range");
+    const TileLoader<kATc, kBTc> load(lds, o);
+    const int lane = load.lane, wm = load.wave / 2, wn = load.wave % 2;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+    const uint32_t a_frag = lds0 + frag_offset<kATc>(wm * 32, lane);
+    const uint32_t b_frag = lds0 + kHalfBytes + frag_offset<kBTc>(wn * 64, lane);
+    const int64_t steps = (o.a.depth + kStepT - 1) / kStepT;
+
+    __builtin_amdgcn_sched_barrier(0);
+    if (fresh) wait_loads<0>();
+    else wait_loads<8 + kStores>();          // step 0; steps 1 and 2 (8) and the stores stay in flight
+    phase_barrier();
+    if (load.wave >= 4) phase_barrier();     // the second four waves run one interval behind
+
+    auto one_step = [&](int64_t step, auto kind) __attribute__((always_inline)) {
+        constexpr int kKind = decltype(kind)::value;  // 0: step 0, 1: step 1, 2: the others
+        bf16x8 fa[1][4];
+        Frags fb;
+        const uint32_t stage = (uint32_t)(step % kSmallStages) * kSmallStageBytes;
+        load.small(step + kSmallStages - 1);          // into the stage of step - 1, which every wave has read
+        read_frags<kBTc>(b_frag + stage, fb);
+        read_block<kATc>(a_frag + stage, fa[0]);
+        wait_loads<8 + (kKind < 2 ? kStores : 0)>();  // step + 1; the two after (8) stay in flight
+        phase_barrier();
+        multiply<kSumA, kKind == 0, 1>(fa, fb, sums.v[0], sums.a_sum[0]);
+        phase_barrier();
+    };
+    if (steps > 0) one_step(0, ActTag<0>{});
+    else clear_sums(sums);
+    if (steps > 1) one_step(1, ActTag<1>{});
+    for (int64_t step = 2; step < steps; ++step) one_step(step, ActTag<2>{});
+    if (load.wave < 4) phase_barrier();
     wait_loads<0>();
     phase_barrier();
 }

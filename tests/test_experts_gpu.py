@@ -67,6 +67,10 @@ SHAPES = [
     ([9, 1, 3, 8, 0, 4], 72, 1096),
     ([0, 5, 1], 136, 16392),
     ([2, 0, 1], 40, 33000),
+    # enough work for the large tiles in the forward, the input's and the weight's gradient
+    ([1500, 0, 700, 257, 1000, 3], 3864, 520),
+    ([1500, 0, 700, 257, 1000, 3], 520, 3864),
+    ([700, 0, 1, 410], 1800, 2000),
 ]
 ACTS = ["silu", "gelu_tanh", "relu", "none"]
 
