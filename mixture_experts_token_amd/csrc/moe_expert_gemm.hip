@@ -201,6 +201,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
         const bool more = id + grid < total;
         const int64_t rows_left = (kWg ? p.m : t.count) - t.r0;
         TileSums<kSmall> sums;
+        clear_sums(sums);
         if (more) next = coord_of(id + grid);  // while the first loads are under way
         tile_sums<kATc, kBTc, kStores, kBiasGrad>(lds, ops, id == slot, rows_left > 128, sums);
         // The next tile's first loads go out ahead of this tile's stores and

@@ -295,8 +295,8 @@ __device__ __forceinline__ float sum8(bf16x8 frag, float v) {
     return v;
 }
 
-// acc += a b over a step, or = with kFirst (no registers to clear before).
-template <bool kSumA, bool kFirst, int kBlocks>
+// acc += a b over a step.
+template <bool kSumA, int kBlocks>
 __device__ __forceinline__ void multiply(const bf16x8 (&a)[kBlocks][4], const Frags& b, f32x16 (&acc)[kBlocks][2],
                                          float (&a_sum)[kBlocks]) {
     __builtin_amdgcn_s_setprio(1);
@@ -306,11 +306,10 @@ __device__ __forceinline__ void multiply(const bf16x8 (&a)[kBlocks][4], const Fr
         for (int f = 0; f < kBlocks; ++f)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-                acc[f][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    b.v[c][s], a[f][s], kFirst && s == 0 ? f32x16{} : acc[f][c], 0, 0, 0);
+                acc[f][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[c][s], a[f][s], acc[f][c], 0, 0, 0);
         if constexpr (kSumA) {
 #pragma unroll
-            for (int f = 0; f < kBlocks; ++f) a_sum[f] = sum8(a[f][s], kFirst && s == 0 ? 0.0f : a_sum[f]);
+            for (int f = 0; f < kBlocks; ++f) a_sum[f] = sum8(a[f][s], a_sum[f]);
         }
     }
     __builtin_amdgcn_s_setprio(0);
@@ -420,9 +419,8 @@ __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool
 
     auto run = [&](auto tag) __attribute__((always_inline)) {
         constexpr bool kBoth = decltype(tag)::value != 0;
-        auto one_step = [&](int64_t step, auto first) __attribute__((always_inline)) {
-            constexpr bool kFirst = decltype(first)::value != 0;
-            constexpr int kExtra = kFirst ? kStores : 0;
+        auto one_step = [&](int64_t step, auto extra) __attribute__((always_inline)) {
+            constexpr int kExtra = decltype(extra)::value;
             Frags fa, fb;
             const uint32_t stage = (uint32_t)(step % 2) * kStageBytes;
             load.a1(step + 1);
@@ -430,20 +428,19 @@ __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool
             read_frags<kATc>(a_frag + stage, fa);
             wait_loads<8 + kExtra>();  // A1 of this step; B, A0 (6) and A1 (2) of the next stay in flight
             phase_barrier();
-            multiply<kSumA, kFirst, 2>(fa.v, fb, sums.v[0], sums.a_sum[0]);
+            multiply<kSumA>(fa.v, fb, sums.v[0], sums.a_sum[0]);
             phase_barrier();
             load.b_a0(step + 2);       // into this stage: every wave has read its B and A0
             if constexpr (kBoth) read_frags<kATc>(a_frag + stage + kHalfBytes, fa);
             wait_loads<8 + kExtra>();  // B, A0 of the next step; its A1 (2) and the B, A0 after (6) stay in flight
             phase_barrier();
-            if constexpr (kBoth) multiply<kSumA, kFirst, 2>(fa.v, fb, sums.v[1], sums.a_sum[1]);
+            if constexpr (kBoth) multiply<kSumA>(fa.v, fb, sums.v[1], sums.a_sum[1]);
             phase_barrier();
         };
-        one_step(0, ActTag<1>{});
+        if (steps > 0) one_step(0, ActTag<kStores>{});
         for (int64_t step = 1; step < steps; ++step) one_step(step, ActTag<0>{});
     };
-    if (steps == 0) clear_sums(sums);  // no rows to sum over
-    else if (second_half) run(ActTag<1>{});
+    if (second_half) run(ActTag<1>{});
     else run(ActTag<0>{});
     if (wm == 0) phase_barrier();
     wait_loads<0>();
@@ -468,23 +465,21 @@ __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool
     phase_barrier();
     if (load.wave >= 4) phase_barrier();     // the second four waves run one interval behind
 
-    auto one_step = [&](int64_t step, auto kind) __attribute__((always_inline)) {
-        constexpr int kKind = decltype(kind)::value;  // 0: step 0, 1: step 1, 2: the others
+    auto one_step = [&](int64_t step, auto extra) __attribute__((always_inline)) {
         bf16x8 fa[1][4];
         Frags fb;
         const uint32_t stage = (uint32_t)(step % kSmallStages) * kSmallStageBytes;
         load.small(step + kSmallStages - 1);          // into the stage of step - 1, which every wave has read
         read_frags<kBTc>(b_frag + stage, fb);
         read_block<kATc>(a_frag + stage, fa[0]);
-        wait_loads<8 + (kKind < 2 ? kStores : 0)>();  // step + 1; the two after (8) stay in flight
+        wait_loads<8 + decltype(extra)::value>();     // step + 1; the two after (8) stay in flight
         phase_barrier();
-        multiply<kSumA, kKind == 0, 1>(fa, fb, sums.v[0], sums.a_sum[0]);
+        multiply<kSumA>(fa, fb, sums.v[0], sums.a_sum[0]);
         phase_barrier();
     };
-    if (steps > 0) one_step(0, ActTag<0>{});
-    else clear_sums(sums);
-    if (steps > 1) one_step(1, ActTag<1>{});
-    for (int64_t step = 2; step < steps; ++step) one_step(step, ActTag<2>{});
+    if (steps > 0) one_step(0, ActTag<kStores>{});
+    if (steps > 1) one_step(1, ActTag<kStores>{});
+    for (int64_t step = 2; step < steps; ++step) one_step(step, ActTag<0>{});
     if (load.wave < 4) phase_barrier();
     wait_loads<0>();
     phase_barrier();
