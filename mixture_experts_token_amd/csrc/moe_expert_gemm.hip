@@ -344,7 +344,13 @@ hipError_t launch_expert_forward(const ExpertForwardArgs& a, int num_cus, hipStr
     p.bias = static_cast<const uint16_t*>(a.bias);
     p.residual = static_cast<const uint16_t*>(a.residual);
     p.pre = static_cast<uint16_t*>(a.pre);
-    const bool small = small_tiles(a.rows.max_rows, most_groups(a.rows), a.n, a.gated ? 128 : 256, a.k, num_cus);
+    // With up to 64 rows per expert the work is streaming the weights, and small
+    // tiles have more of them in flight (8 to 64 rows per expert, small / large
+    // us: 14336 x 4096 gated, 8 experts 355 / 401; 4096 x 14336 164 / 257;
+    // 768 x 2048 gated, 128 experts 181 / 191; 2048 x 768 96 / 91).
+    const int64_t groups = most_groups(a.rows);
+    const bool small = a.rows.max_rows <= 64 * groups ||
+                       small_tiles(a.rows.max_rows, groups, a.n, a.gated ? 128 : 256, a.k, num_cus);
     return with_activation(a.activation, [&](auto act) {
         constexpr int kAct = decltype(act)::value;
         return a.gated ? launch_product<Product::kForward, true, kAct>(p, small, num_cus, stream)

@@ -225,18 +225,18 @@ int x_rows_in(int lds_bytes, int64_t k) {
 
 }  // namespace
 
-// Where this kernel beats the tiled one (us at r rows per expert, this / tiled;
-// n x k of the layer):
-//   8 x rows fit, rows of 1024 or more: up to 6 rows per expert.  14336 x 4096
-//     gated, 8 experts: r 2 215 / 281, 4 270 / 370, 6 339 / 397, 8 433 / 396;
-//     768 x 2048 gated, 128 experts: 4 136 / 182, 6 165 / 186, 8 211 / 189;
-//     7168 x 2048, 64 experts: 4 305 / 406, 6 367 / 410, 8 448 / 412.
-//   otherwise up to 3.  4096 x 14336 (two x rows fit): 2 157 / 252, 3 204 / 250,
-//     4 254 / 251; 2048 x 7168 gated (four): 2 491 / 595, 3 615 / 609, 4 734 / 623;
-//     2048 x 768: 2 69 / 83, 3 86 / 86, 4 103 / 87.
+// Where this kernel beats the tiled ones (us at r rows per expert, this / tiled;
+// n x k of the layer): up to
+//   6 rows per expert where 8 x rows of at least 1024 fit.  14336 x 4096 gated, 8
+//     experts: r 2 215 / 281, 4 268 / 355, 6 336 / 355, 8 433 / 355; 768 x 2048
+//     gated, 128 experts: 4 137 / 179, 6 164 / 179, 8 211 / 179; 7168 x 2048, 64
+//     experts: 4 303 / 392, 6 363 / 392, 8 448 / 392.
+//   3 where 4 fit, or shorter rows.  2048 x 7168 gated: 2 493 / 595, 3 618 / 609,
+//     4 734 / 623; 2048 x 768: 2 71 / 83, 3 88 / 86, 4 103 / 95.
+//   2 otherwise.  4096 x 14336 (two fit): 1 112 / 147, 2 157 / 147, 3 205 / 147.
 bool expert_stream_applies(const ExpertForwardArgs& a) {
     const int x = x_rows_in(kLargeLds, a.k);
-    const int64_t rows_per_expert = x == kMaxX && a.k >= 1024 ? 6 : 3;
+    const int64_t rows_per_expert = x == kMaxX && a.k >= 1024 ? 6 : x >= 4 ? 3 : 2;
     return x >= 1 && a.rows.max_rows <= rows_per_expert * a.rows.num_experts;
 }
 
