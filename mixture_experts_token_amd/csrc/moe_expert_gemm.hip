@@ -98,7 +98,9 @@ __device__ __forceinline__ void for_each_block(int wm, F&& f) {
         for (int fb = 0; fb < S::kBlocks; ++fb) f(h, fb, h * 128 + wm * 32 * S::kBlocks + fb * 32);
 }
 
-// A block's sums, rounded, into `dst` at (row, col).
+// A block's sums, rounded, into `dst` at (row, col).  The weights' gradient is
+// streamed: it is larger than what the caches hold of the other operands.
+template <bool kStream = false>
 __device__ __forceinline__ void store_block(const WaveBlock& block, const TileMatrix& dst, int row, int col, int lane,
                                             const f32x16& v) {
     u32x2 runs[4];
@@ -107,7 +109,7 @@ __device__ __forceinline__ void store_block(const WaveBlock& block, const TileMa
     for (int j = 0; j < 4; ++j)
         runs[j] = u32x2{pack_bf16(v[4 * j], v[4 * j + 1]), pack_bf16(v[4 * j + 2], v[4 * j + 3])};
     block.to_vectors(runs, out);
-    dst.store(row, col, lane, out);
+    dst.store<kStream>(row, col, lane, out);
 }
 
 __device__ __forceinline__ void add4(f32x16& v, int j, u32x2 w) {
@@ -209,6 +211,10 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
         if (more) {
             ops = operands_of(next);
             begin_tile<kSmall, kATc, kBTc>(lds, ops);
+            // with a short T, the stores of the first waves would delay the
+            // others' loads (128 experts of 512 rows, 1536 x 2048: 1 % of both
+            // gradients; no gain in the other products)
+            if constexpr (kWg) phase_barrier();
         }
 
         const int lane = opaque_lane();
@@ -272,7 +278,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
 #pragma unroll
                 for (int cb = 0; cb < 2; ++cb)
                     for_each_block<S>(wm, [&](int h, int f, int r) {
-                        store_block(block, out, r, wn * 64 + cb * 32, lane, sums.v[h][f][cb]);
+                        store_block<kWg>(block, out, r, wn * 64 + cb * 32, lane, sums.v[h][f][cb]);
                     });
             }
         }

@@ -556,11 +556,13 @@ struct TileMatrix {
         return (int)(col < cols ? (uint32_t)row * row_bytes + (uint32_t)col * 2 : kOutOfRange);
     }
     // The two vectors of the 32 x 32 block at (row, col) that WaveBlock gives this lane.
+    // kStream: stored non-temporally (nothing reads them soon).
+    template <bool kStream>
     __device__ __forceinline__ void store(int row, int col, int lane, const u32x4 (&v)[2]) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             __builtin_amdgcn_raw_buffer_store_b128(v[i], rsrc, offset(row + i * 16 + lane / 4, col + lane % 4 * 8), 0,
-                                                   0);
+                                                   kStream ? 2 : 0);
     }
     __device__ __forceinline__ void load(int row, int col, int lane, u32x4 (&v)[2]) const {
 #pragma unroll
