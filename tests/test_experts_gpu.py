@@ -71,6 +71,7 @@ SHAPES = [
     ([1500, 0, 700, 257, 1000, 3], 3864, 520),
     ([1500, 0, 700, 257, 1000, 3], 520, 3864),
     ([700, 0, 1, 410], 1800, 2000),
+    ([128, 384, 385, 256, 0, 641], 2056, 1288),
 ]
 ACTS = ["silu", "gelu_tanh", "relu", "none"]
 
@@ -269,6 +270,80 @@ def test_masked_rows_infinities_stay_in_their_rows(hip_device):
     keep = [i for i in range(110) if i not in (7, 50)]
     assert torch.equal(_bits(clean[keep]), _bits(dirty[keep]))
     assert not torch.isfinite(dirty[50].float()).any()
+
+
+@pytest.mark.parametrize("shape", [SHAPES[3], SHAPES[-1]], ids=_id)
+def test_repeated_calls_give_the_same_bits(hip_device, shape):
+    """No sum depends on timing: three calls, the same bits."""
+    counts, n, k = shape
+    dev = hip_device
+    m, e = sum(counts), len(counts)
+    off, x = offsets(counts, dev), rows_of(counts, k, 1, dev)
+    w, d_y = randn((e, n, k), 2, dev, k**-0.5), rows_of(counts, n, 3, dev)
+    first = None
+    for _ in range(3):
+        outs = [poisoned((m + TAIL, n), BF16, dev), poisoned((m + TAIL, k), BF16, dev), poisoned((e, n, k), BF16, dev),
+                poisoned((e, n), BF16, dev)]
+        moe.moe_grouped_linear_bf16(x, w, off, outs[0])
+        moe.moe_grouped_linear_backward_bf16(d_y, x, w, off, d_x=outs[1], d_w=outs[2], d_bias=outs[3])
+        torch.cuda.synchronize()
+        bits = [_bits(t) for t in outs]
+        first = first or bits
+        assert all(torch.equal(a, b) for a, b in zip(first, bits))
+
+
+def test_row_offsets_past_32_bits(hip_device):
+    """600001 rows of 4096: elements pass 2^31 and bytes 2^32; a k-loop of 300000 rows."""
+    dev = hip_device
+    counts, n, k = [300000, 300001], 64, 4096
+    m = sum(counts)
+    _say("row offsets past 32 bits: %d rows of %d" % (m, k))
+    g = torch.Generator(device=dev).manual_seed(1)
+    x = torch.randn(m, k, generator=g, device=dev, dtype=BF16)
+    w, off = randn((2, n, k), 2, dev, k**-0.5), offsets(counts, dev)
+    d_y = torch.randn(m, n, generator=g, device=dev, dtype=BF16)
+    y, d_x = poisoned((m, n), BF16, dev), poisoned((m, k), BF16, dev)
+    d_w, d_b = poisoned((2, n, k), BF16, dev), poisoned((2, n), BF16, dev)
+    moe.moe_grouped_linear_bf16(x, w, off, y)
+    moe.moe_grouped_linear_backward_bf16(d_y, x, w, off, d_x=d_x, d_w=d_w, d_bias=d_b)
+    torch.cuda.synchronize()
+    pick = torch.tensor([0, 1, 255, 256, 299998, 299999, 300000, 300001, 524287, 524288, 599999, 600000], device=dev)
+    part = torch.tensor([0, 6, 12])
+    X.check_linear(x[pick], w, None, None, part, "none", y[pick], None)
+    X.check_products(d_y[pick], None, w, part, d_x[pick], None)
+    for e, lo, hi in X.segments(off.cpu()):
+        ref, mag = torch.zeros(n, k, dtype=torch.float64, device=dev), torch.zeros(n, k, dtype=torch.float64, device=dev)
+        ref_b, mag_b = 0.0, 0.0
+        for at in range(lo, hi, 20000):
+            rows = slice(at, min(at + 20000, hi))
+            d, xs = d_y[rows].double().t().contiguous(), x[rows].double()
+            ref += torch.mm(d, xs)
+            mag += torch.mm(d.abs(), xs.abs())
+            ref_b, mag_b = ref_b + d.sum(1), mag_b + d.abs().sum(1)
+        t = X.accumulate(hi - lo)
+        X.assert_within(d_w[e], ref.cpu(), X.HALF * ref.abs().cpu() + t * mag.cpu(), "d_w")
+        X.assert_within(d_b[e], ref_b.cpu(), X.HALF * ref_b.abs().cpu() + t * mag_b.cpu(), "d_bias")
+
+
+def test_unpermute_backward_past_32_bits(hip_device):
+    dev = hip_device
+    n, k, h = 150000, 2, 8192
+    _say("unpermute backward past 32 bits: %d rows of %d" % (n * k, h))
+    g = torch.Generator(device=dev).manual_seed(1)
+    d_out = torch.randn(n, h, generator=g, device=dev, dtype=BF16)
+    y = torch.randn(n * k, h, generator=g, device=dev, dtype=BF16)
+    wts = torch.rand(n, k, generator=g, device=dev)
+    inv = torch.randperm(n * k, generator=g, device=dev).int()
+    d_y, d_w = poisoned((n * k, h), BF16, dev), poisoned((n, k), torch.float32, dev)
+    moe.moe_unpermute_backward(d_out, y, wts, inv, d_expanded_output=d_y, d_topk_weights=d_w)
+    torch.cuda.synchronize()
+    for t in (0, 1, 77777, n - 2, n - 1):
+        for i in range(k):
+            j = int(inv[t * k + i])
+            ref = X.f64(wts[t, i]) * X.f64(d_out[t])
+            X.assert_within(d_y[j], ref, (X.HALF + 2.0**-24) * ref.abs(), "row %d" % j)
+            prod = X.f64(d_out[t]) * X.f64(y[j])
+            X.assert_within(d_w[t, i:i + 1], prod.sum()[None], X.accumulate(h) * prod.abs().sum()[None], "weight")
 
 
 # ------------------------------------------------------------ unpermute backward
