@@ -84,6 +84,10 @@ bool expert_stream_applies(const ExpertForwardArgs& a);
 hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, hipStream_t stream);
 hipError_t launch_expert_input_grad(const ExpertInputGradArgs& a, int num_cus, hipStream_t stream);
 hipError_t launch_expert_weight_grad(const ExpertWeightGradArgs& a, int num_cus, hipStream_t stream);
+// The weight gradient of the experts with at most kOuterRows rows, and of those alone (called by
+// launch_expert_weight_grad, whose matrix kernel then leaves them out).
+constexpr int kOuterRows = 16;
+hipError_t launch_expert_outer(const ExpertWeightGradArgs& a, int num_cus, hipStream_t stream);
 hipError_t launch_expert_act_grad(const ExpertActGradArgs& a, int num_cus, hipStream_t stream);
 hipError_t launch_expert_bias_grad(const ExpertBiasGradArgs& a, hipStream_t stream);
 hipError_t launch_unpermute_backward(const UnpermuteBackwardArgs& a, bool bf16, hipStream_t stream);

@@ -67,6 +67,10 @@ SHAPES = [
     ([9, 1, 3, 8, 0, 4], 72, 1096),
     ([0, 5, 1], 136, 16392),
     ([2, 0, 1], 40, 33000),
+    # experts on both sides of the weight gradient's row limit, rows of whole
+    # lines and not, more columns than one of its items
+    ([16, 17, 0, 2, 15, 8, 1, 4, 40], 72, 2176),
+    ([16, 17, 0, 2, 15, 8, 1, 4, 40], 264, 2120),
     # enough work for the large tiles in the forward, the input's and the weight's gradient
     ([1500, 0, 700, 257, 1000, 3], 3864, 520),
     ([1500, 0, 700, 257, 1000, 3], 520, 3864),
