@@ -34,6 +34,7 @@ constexpr int64_t kGroupRows = 8;  // row tiles per group in the tile order
 // Cost of a tile outside its k-loop, and of a small tile's step, in steps of a
 // large one (1.5 us with every CU busy; 10 us and 0.6 - 0.7 us measured).
 constexpr double kFixedCost = 6.0, kSmallStepCost = 0.45, kSmallFixedCost = 3.0;
+constexpr int64_t kApartMostRounds = 4;
 
 struct GemmParams {
     const int64_t* off;
@@ -46,6 +47,7 @@ struct GemmParams {
     const uint16_t* bias;
     const uint16_t* residual;
     uint16_t* pre;
+    bool apart;                // light remainders may go to a launch of small tiles (remainders_apart)
     int64_t skip_rows;         // weight grad: experts with up to that many rows are left out (-1: none)
     bool stream_out;           // weight grad: whole lines, stored non-temporally
     uint16_t* d_bias;          // [num_experts, m] (weight and bias grad)
@@ -68,18 +70,55 @@ struct TileCoord {
     int64_t r0, c0;        // the tile's first output row (of the expert's) and column
 };
 
+// An expert's remainder of at most half a large tile's rows.
+__device__ __forceinline__ bool light_remainder(int64_t count) {
+    const int64_t left = count % TileShape<false>::kRows;
+    return left > 0 && left <= TileShape<true>::kRows;
+}
+
+// Which of an expert's rows a launch takes.
+enum class Part { kAll, kNoLight, kLight };
+
+template <int kRows>
+__device__ __forceinline__ int64_t row_tiles(int64_t rows, Part part) {
+    if (part == Part::kLight) return light_remainder(rows) ? 1 : 0;
+    return (rows + kRows - 1) / kRows - (part == Part::kNoLight && light_remainder(rows) ? 1 : 0);
+}
+
+// Whether the tiles of the light remainders (light of them, beside heavy others)
+// are better taken as small tiles by a launch of their own: with few rounds of
+// workgroups, a last one of only some light tiles leaves most CUs idle for as
+// long as a whole tile takes (512 heavy and 64 light tiles of 224 steps, 256
+// CUs: 987 us in one launch, 891 in two).  Both launches ask this.  Costs in
+// hundredths of a step, as choose_tiles has them; past a few rounds the light
+// tiles fill gaps, and apart they would stream the weights again.
+__device__ __forceinline__ bool remainders_apart(int64_t heavy, int64_t light, int64_t depth, int64_t cus) {
+    if (light == 0 || heavy > kApartMostRounds * cus) return false;
+    const int64_t steps = (depth + kStepT - 1) / kStepT;
+    const int64_t large = steps * 100 + (int64_t)(kFixedCost * 100);
+    const int64_t small = (int64_t)(kSmallStepCost * 100) * steps + (int64_t)(kSmallFixedCost * 100);
+    const int64_t together = (heavy + light + cus - 1) / cus * large;
+    const int64_t split = (heavy + cus - 1) / cus * large + (2 * light + cus - 1) / cus * small;
+    return split < together / 10 * 9;
+}
+
 // Order of an expert's tiles: groups of kGroupRows row tiles, within a group
 // row tiles fastest, then column tiles; a remainder of up to three row tiles
 // joins the last group (it would stream every column tile again for itself).
 template <bool kWeightGrad, int kRows>
 __device__ __forceinline__ TileCoord tile_coord(int64_t id, const int64_t* pre, const int64_t* off, int num_experts,
-                                                int64_t m, int64_t col_tiles, int cols_per_tile) {
+                                                int64_t m, int64_t col_tiles, int cols_per_tile, Part part) {
     TileCoord t;
     t.expert = expert_of_item(pre, num_experts, id);
     t.first = wave_uniform64(off[t.expert]);
     t.count = wave_uniform64(off[t.expert + 1]) - t.first;
     const int64_t local = id - wave_uniform64(pre[t.expert]);
-    const int64_t mt = ((kWeightGrad ? m : t.count) + kRows - 1) / kRows;
+    if (part == Part::kLight) {
+        t.r0 = wave_uniform64(t.count / TileShape<false>::kRows * TileShape<false>::kRows);
+        t.c0 = wave_uniform64(local * cols_per_tile);
+        return t;
+    }
+    const int64_t mt = row_tiles<kRows>(kWeightGrad ? m : t.count, part);
     const int64_t left = mt % kGroupRows;
     const int64_t groups = mt / kGroupRows + (left > 3 || mt < kGroupRows);
     int64_t rem;
@@ -131,13 +170,31 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
     __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
     __shared__ __attribute__((aligned(1024))) char blocks[kTileThreads / 64 * kBlockBytes];
     __shared__ int64_t pre_s[kMaxExperts + 1];
-    __shared__ int64_t part[kTileThreads / 64];
+    __shared__ int64_t part_s[kTileThreads / 64];
     const int64_t cols = kP == Product::kForward ? p.n : p.k;
     const int64_t col_tiles = (cols + kColsPerTile - 1) / kColsPerTile;
-    const bool ok = expert_items<kTileThreads>(p.off, p.num_experts, p.max_rows, pre_s, part, [&](int64_t rows) {
+    Part part = Part::kAll;
+    if (!kWg && p.apart) {
+        // in large tiles, whichever this launch has
+        constexpr int kLargeCols = kGated ? 128 : 256;
+        const int64_t large_cols = (cols + kLargeCols - 1) / kLargeCols;
+        if (!expert_items<kTileThreads>(p.off, p.num_experts, p.max_rows, pre_s, part_s,
+                                        [&](int64_t rows) { return light_remainder(rows) ? large_cols : 0; }))
+            return;
+        const int64_t light = pre_s[p.num_experts];
+        __syncthreads();
+        expert_items<kTileThreads>(p.off, p.num_experts, p.max_rows, pre_s, part_s, [&](int64_t rows) {
+            return row_tiles<TileShape<false>::kRows>(rows, Part::kNoLight) * large_cols;
+        });
+        const int64_t heavy = pre_s[p.num_experts];
+        __syncthreads();
+        const bool apart = remainders_apart(heavy, light, kP == Product::kForward ? p.k : p.m, gridDim.x);
+        if (kSmall && !apart) return;  // the launch before took them
+        if (apart) part = kSmall ? Part::kLight : Part::kNoLight;
+    }
+    const bool ok = expert_items<kTileThreads>(p.off, p.num_experts, p.max_rows, pre_s, part_s, [&](int64_t rows) {
         if (kWg && rows <= p.skip_rows) return (int64_t)0;
-        const int64_t r = kWg ? p.m : rows;
-        return (r + S::kRows - 1) / S::kRows * col_tiles;
+        return row_tiles<S::kRows>(kWg ? p.m : rows, part) * col_tiles;
     });
     if (!ok) return;
     const int64_t total = wave_uniform64(pre_s[p.num_experts]);
@@ -191,7 +248,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
         return o;
     };
     auto coord_of = [&](int64_t id) __attribute__((always_inline)) {
-        return tile_coord<kWg, S::kRows>(id, pre_s, p.off, p.num_experts, p.m, col_tiles, kColsPerTile);
+        return tile_coord<kWg, S::kRows>(id, pre_s, p.off, p.num_experts, p.m, col_tiles, kColsPerTile, part);
     };
     // Stores of every tile at least (vectors of its outputs, per lane).
     constexpr int kStores = S::kHalves * S::kBlocks * (kGated ? 2 : 4);
@@ -304,20 +361,34 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
     }
 }
 
+struct TileChoice {
+    bool small;   // 128 x 128 tiles
+    bool apart;   // large ones, with the light remainders perhaps in a launch of their own
+};
+
 // Whether a product runs faster on small tiles: its rounds of workgroups times
 // what a tile takes.  rows: output rows of all experts; groups: experts that may
 // have rows (each ends in half a tile on average).  Small / large tiles, us:
 // one expert 1024^3 18.1 / 27.9, 2048^3 29 / 54, 4096 x 4096 x 512 37.7 / 26.1;
 // 8 experts of 300 rows, 1024 x 1024 18 / 29.5, of 1024, 2048 x 2048 125 / 104;
 // 128 of 64, 768 x 2048 112 / 127, of 128 144 / 134.
-bool small_tiles(int64_t rows, int64_t groups, int64_t cols, int64_t cols_large, int64_t depth, int num_cus) {
-    auto cost = [&](int64_t tile, int64_t tile_cols, double step, double fixed) {
+TileChoice choose_tiles(int64_t rows, int64_t groups, int64_t cols, int64_t cols_large, int64_t depth, int num_cus) {
+    const int64_t steps = (depth + kStepT - 1) / kStepT;
+    auto rounds = [&](int64_t tile, int64_t tile_cols) {
         const int64_t row_tiles = (rows + tile - 1) / tile + (groups > 1 ? (groups - 1) / 2 : 0);
         const int64_t tiles = row_tiles * ((cols + tile_cols - 1) / tile_cols);
-        const int64_t rounds = (tiles + num_cus - 1) / num_cus;
-        return (double)rounds * ((double)((depth + kStepT - 1) / kStepT) * step + fixed);
+        return (tiles + num_cus - 1) / num_cus;
     };
-    return cost(128, cols_large / 2, kSmallStepCost, kSmallFixedCost) < cost(256, cols_large, 1.0, kFixedCost);
+    const int64_t large = rounds(256, cols_large);
+    TileChoice c;
+    c.small = (double)rounds(128, cols_large / 2) * ((double)steps * kSmallStepCost + kSmallFixedCost) <
+              (double)large * ((double)steps + kFixedCost);
+    // The second launch and its test cost some 7 us where it finds nothing to do;
+    // with fewer than three whole tiles per expert the light tiles' weights weigh
+    // more than the idle CUs (32 experts of 300 rows, 768 x 2048 gated: 92 us in
+    // one launch, 113 in two; 8 of 1024, 2048 x 2048: 99 / 92).
+    c.apart = !c.small && groups > 1 && rows >= 768 * groups && large <= kApartMostRounds + 1 && steps >= 16;
+    return c;
 }
 
 template <Product kP, bool kGated, int kAct>
@@ -325,6 +396,9 @@ hipError_t launch_product(const GemmParams& p, bool small, int num_cus, hipStrea
     const int blocks = num_cus < kXcdCount ? kXcdCount : num_cus / kXcdCount * kXcdCount;
     auto* kernel = small ? expert_product_kernel<kP, kGated, kAct, true> : expert_product_kernel<kP, kGated, kAct, false>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kTileThreads), 0, stream, p);
+    if (p.apart && hipPeekAtLastError() == hipSuccess)
+        hipLaunchKernelGGL((expert_product_kernel<kP, kGated, kAct, true>), dim3((unsigned)blocks), dim3(kTileThreads),
+                           0, stream, p);
     return hipGetLastError();
 }
 
@@ -359,19 +433,21 @@ hipError_t launch_expert_forward(const ExpertForwardArgs& a, int num_cus, hipStr
     // us: 14336 x 4096 gated, 8 experts 355 / 401; 4096 x 14336 164 / 257;
     // 768 x 2048 gated, 128 experts 181 / 191; 2048 x 768 96 / 91).
     const int64_t groups = most_groups(a.rows);
-    const bool small = a.rows.max_rows <= 64 * groups ||
-                       small_tiles(a.rows.max_rows, groups, a.n, a.gated ? 128 : 256, a.k, num_cus);
+    TileChoice tiles = choose_tiles(a.rows.max_rows, groups, a.n, a.gated ? 128 : 256, a.k, num_cus);
+    if (a.rows.max_rows <= 64 * groups) tiles = {true, false};
+    p.apart = tiles.apart;
     return with_activation(a.activation, [&](auto act) {
         constexpr int kAct = decltype(act)::value;
-        return a.gated ? launch_product<Product::kForward, true, kAct>(p, small, num_cus, stream)
-                       : launch_product<Product::kForward, false, kAct>(p, small, num_cus, stream);
+        return a.gated ? launch_product<Product::kForward, true, kAct>(p, tiles.small, num_cus, stream)
+                       : launch_product<Product::kForward, false, kAct>(p, tiles.small, num_cus, stream);
     });
 }
 
 hipError_t launch_expert_input_grad(const ExpertInputGradArgs& a, int num_cus, hipStream_t stream) {
-    const bool small = small_tiles(a.rows.max_rows, most_groups(a.rows), a.k, 256, a.m, num_cus);
-    return launch_product<Product::kInputGrad, false, kActNone>(params_of(a.rows, a.m, a.k, a.d_z, a.w, a.d_x), small,
-                                                                num_cus, stream);
+    GemmParams p = params_of(a.rows, a.m, a.k, a.d_z, a.w, a.d_x);
+    const TileChoice tiles = choose_tiles(a.rows.max_rows, most_groups(a.rows), a.k, 256, a.m, num_cus);
+    p.apart = tiles.apart;
+    return launch_product<Product::kInputGrad, false, kActNone>(p, tiles.small, num_cus, stream);
 }
 
 constexpr int64_t kOuterMostAverage = 64;
@@ -397,7 +473,7 @@ hipError_t launch_expert_weight_grad(const ExpertWeightGradArgs& a, int num_cus,
     }
     // every expert has all its tiles; T is its share of the rows
     const int64_t e = a.rows.num_experts;
-    const bool small = small_tiles(a.m * e, 0, a.k, 256, a.rows.max_rows / e + 1, num_cus);
+    const bool small = choose_tiles(a.m * e, 0, a.k, 256, a.rows.max_rows / e + 1, num_cus).small;
     return p.d_bias != nullptr ? launch_product<Product::kWeightBiasGrad, false, kActNone>(p, small, num_cus, stream)
                                : launch_product<Product::kWeightGrad, false, kActNone>(p, small, num_cus, stream);
 }

@@ -76,6 +76,9 @@ SHAPES = [
     ([1500, 0, 700, 257, 1000, 3], 520, 3864),
     ([700, 0, 1, 410], 1800, 2000),
     ([128, 384, 385, 256, 0, 641], 2056, 1288),
+    # 256 heavy large tiles and the remainders of two experts beside them (forward; input's gradient)
+    ([1024, 1025, 1134, 1023], 3960, 1032),
+    ([1024, 1025, 1134, 1023], 1032, 3960),
 ]
 ACTS = ["silu", "gelu_tanh", "relu", "none"]
 
