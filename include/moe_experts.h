@@ -66,8 +66,8 @@ moe_status_t moe_grouped_gated_gemm_bf16(const void *x, const void *w, const int
  *     d_x[j][i]    = sum_c d_gate_up[j][c] * w[e][c][i]         over the 2 n columns
  *     d_w[e][c][i] = sum_j d_gate_up[j][c] * x[j][i]            over the rows j of e
  * The products take the bf16 d_gate_up: the matrix cores multiply bf16, and
- * its rounding (half a step, 2^-9 relative on average over a sum of many
- * terms) is of the size of the rounding of the results themselves.
+ * its rounding (at most 2^-8 of a value, of either sign over a sum) is of the
+ * size of the rounding of the results themselves.
  *
  *   d_h        [max_rows, n] bf16      gate_up [max_rows, 2 n] bf16, as the forward wrote it
  *   x, w       as in the forward; x may be NULL without d_w, w without d_x

@@ -48,7 +48,7 @@ struct GemmParams {
     const uint16_t* residual;
     uint16_t* pre;
     bool apart;                // light remainders may go to a launch of small tiles (remainders_apart)
-    int64_t skip_rows;         // weight grad: experts with up to that many rows are left out (-1: none)
+    int64_t skip_rows;         // experts with up to that many rows are left out (-1: none)
     bool stream_out;           // weight grad: whole lines, stored non-temporally
     uint16_t* d_bias;          // [num_experts, m] (weight and bias grad)
     uint16_t* out;
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void expert_product_kernel(GemmPar
         if (apart) part = kSmall ? Part::kLight : Part::kNoLight;
     }
     const bool ok = expert_items<kTileThreads>(p.off, p.num_experts, p.max_rows, pre_s, part_s, [&](int64_t rows) {
-        if (kWg && rows <= p.skip_rows) return (int64_t)0;
+        if (rows <= p.skip_rows) return (int64_t)0;
         return row_tiles<S::kRows>(kWg ? p.m : rows, part) * col_tiles;
     });
     if (!ok) return;
@@ -413,6 +413,7 @@ GemmParams params_of(const ExpertRows& rows, int64_t m, int64_t k, const void* a
     p.m = m;
     p.k = k;
     p.n = m;
+    p.skip_rows = -1;
     p.a = static_cast<const uint16_t*>(a);
     p.b = static_cast<const uint16_t*>(b);
     p.out = static_cast<uint16_t*>(out);
@@ -422,8 +423,12 @@ GemmParams params_of(const ExpertRows& rows, int64_t m, int64_t k, const void* a
 }  // namespace
 
 hipError_t launch_expert_forward(const ExpertForwardArgs& a, int num_cus, hipStream_t stream) {
-    if (expert_stream_applies(a)) return launch_expert_stream(a, num_cus, stream);
     GemmParams p = params_of(a.rows, a.gated ? 2 * a.n : a.n, a.k, a.x, a.w, a.y);
+    const bool streamed = expert_stream_applies(a);
+    if (streamed) {
+        const hipError_t err = launch_expert_stream(a, num_cus, &p.skip_rows, stream);
+        if (err != hipSuccess || a.rows.max_rows <= p.skip_rows) return err;  // no expert can have more
+    }
     p.n = a.n;
     p.bias = static_cast<const uint16_t*>(a.bias);
     p.residual = static_cast<const uint16_t*>(a.residual);
@@ -434,7 +439,7 @@ hipError_t launch_expert_forward(const ExpertForwardArgs& a, int num_cus, hipStr
     // 768 x 2048 gated, 128 experts 181 / 191; 2048 x 768 96 / 91).
     const int64_t groups = most_groups(a.rows);
     TileChoice tiles = choose_tiles(a.rows.max_rows, groups, a.n, a.gated ? 128 : 256, a.k, num_cus);
-    if (a.rows.max_rows <= 64 * groups) tiles = {true, false};
+    if (streamed || a.rows.max_rows <= 64 * groups) tiles = {true, false};
     p.apart = tiles.apart;
     return with_activation(a.activation, [&](auto act) {
         constexpr int kAct = decltype(act)::value;
@@ -465,7 +470,6 @@ hipError_t launch_expert_weight_grad(const ExpertWeightGradArgs& a, int num_cus,
     // rows fall is not known here, and a launch that finds no such expert costs 6
     // us, so past 64 rows per expert on average it is left out (32 experts of 512
     // rows of which 4 have none: 1 % slower without; 128 of 512: 1 % faster).
-    p.skip_rows = -1;
     if (a.rows.max_rows <= kOuterMostAverage * a.rows.num_experts) {
         const hipError_t err = launch_expert_outer(a, num_cus, stream);
         if (err != hipSuccess || a.rows.max_rows <= kOuterRows) return err;

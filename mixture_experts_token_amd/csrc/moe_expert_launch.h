@@ -79,9 +79,10 @@ struct UnpermuteBackwardArgs {
 };
 
 hipError_t launch_expert_forward(const ExpertForwardArgs& a, int num_cus, hipStream_t stream);
-// The forward for experts with few rows each (called by launch_expert_forward where it applies).
+// The forward for experts with few rows each (called by launch_expert_forward where it applies); experts
+// with more than most_rows (out) rows are left to the tiled kernel.
 bool expert_stream_applies(const ExpertForwardArgs& a);
-hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, hipStream_t stream);
+hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, int64_t* most_rows, hipStream_t stream);
 hipError_t launch_expert_input_grad(const ExpertInputGradArgs& a, int num_cus, hipStream_t stream);
 hipError_t launch_expert_weight_grad(const ExpertWeightGradArgs& a, int num_cus, hipStream_t stream);
 // The weight gradient of the experts with at most kOuterRows rows, and of those alone (called by

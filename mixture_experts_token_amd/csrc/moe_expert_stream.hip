@@ -38,6 +38,7 @@ struct StreamParams {
     int64_t max_rows;
     int64_t n, k;               // output columns, row length
     int x_rows;                 // x rows per item
+    int64_t most_rows;          // experts with more rows are left out
     const u32x4* x;
     const uint16_t* w;
     const uint16_t* bias;
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(kStreamThreads, 4) void expert_stream_kernel(Stream
     constexpr int kItemCols = kStreamWaves * kWaveCols;
     const int64_t blocks = (p.n + kItemCols - 1) / kItemCols;
     const bool ok = expert_items<kStreamThreads>(p.off, p.num_experts, p.max_rows, pre_s, part, [&](int64_t rows) {
-        return (rows + p.x_rows - 1) / p.x_rows * blocks;
+        return rows > p.most_rows ? 0 : (rows + p.x_rows - 1) / p.x_rows * blocks;
     });
     if (!ok) return;
     const int lane = threadIdx.x % 64;
@@ -240,7 +241,13 @@ bool expert_stream_applies(const ExpertForwardArgs& a) {
     return x >= 1 && a.rows.max_rows <= rows_per_expert * a.rows.num_experts;
 }
 
-hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, hipStream_t stream) {
+// An expert of many rows would have its weights streamed once per x_rows of
+// them: past four times that the tiled kernel takes it (64 experts, 2048 x 4096
+// gated, rows 120, 50, 30, 20 and 40 times 3: 370 -> 292 us; its launch costs
+// 6 - 9 us where no expert has that many).  With up to two rows per expert on
+// average all are streamed: that is never more than one of four experts' weights
+// beside what evenly spread rows read.
+hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, int64_t* most_rows, hipStream_t stream) {
     StreamParams p{};
     p.off = a.rows.offsets;
     p.num_experts = a.rows.num_experts;
@@ -256,6 +263,7 @@ hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, hipStre
     // A row per expert or fewer: two x rows an item, and twice the workgroups.
     const bool small = a.rows.max_rows <= a.rows.num_experts && x_rows_in(kSmallLds, a.k) >= 2;
     p.x_rows = x_rows_in(small ? kSmallLds : kLargeLds, a.k);
+    p.most_rows = *most_rows = a.rows.max_rows <= 2 * (int64_t)a.rows.num_experts ? a.rows.max_rows : 4 * (int64_t)p.x_rows;
     return with_activation(a.activation, [&](auto act) {
         constexpr int kAct = decltype(act)::value;
         if (a.gated)

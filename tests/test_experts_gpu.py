@@ -67,6 +67,8 @@ SHAPES = [
     ([9, 1, 3, 8, 0, 4], 72, 1096),
     ([0, 5, 1], 136, 16392),
     ([2, 0, 1], 40, 33000),
+    # one expert with most of the rows beside many with few (streamed and tiled in one call)
+    ([1, 0, 2] * 15 + [190, 33, 32], 136, 1096),
     # experts on both sides of the weight gradient's row limit, rows of whole
     # lines and not, more columns than one of its items
     ([16, 17, 0, 2, 15, 8, 1, 4, 40], 72, 2176),
