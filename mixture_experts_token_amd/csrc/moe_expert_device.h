@@ -116,9 +116,10 @@ __device__ __forceinline__ bool expert_items(const int64_t* __restrict__ off, in
         const int e = tid * kPer + q;
         cnt[q] = 0;
         if (e < num_experts) {
-            const int64_t rows = off[e + 1] - off[e];
-            bad |= rows < 0;
-            cnt[q] = rows >= 0 ? items(rows) : 0;
+            const int64_t first = off[e], last = off[e + 1];
+            const bool falls = last < first;  // compared, not subtracted: a difference can wrap
+            bad |= falls;
+            cnt[q] = falls ? 0 : items((int64_t)((uint64_t)last - (uint64_t)first));
         }
         s += cnt[q];
     }

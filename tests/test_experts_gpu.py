@@ -207,7 +207,8 @@ def test_no_rows_at_all(hip_device):
     assert not d_w.any() and not d_b.any()
 
 
-BAD_OFFSETS = [[0, 5, 3, 9], [1, 3, 5, 9], [0, 3, 5, 400], [-1, -1, -1, -1], [0, 3, -2, 9]]
+# the last: every difference is positive once it wraps around 2^64
+BAD_OFFSETS = [[0, 5, 3, 9], [1, 3, 5, 9], [0, 3, 5, 400], [-1, -1, -1, -1], [0, 3, -2, 9], [0, 2**63 - 1, -2, 9]]
 
 
 @pytest.mark.parametrize("off", BAD_OFFSETS, ids=str)
