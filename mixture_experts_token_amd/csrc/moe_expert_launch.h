@@ -85,6 +85,9 @@ bool expert_stream_applies(const ExpertForwardArgs& a);
 hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, int64_t* most_rows, hipStream_t stream);
 hipError_t launch_expert_input_grad(const ExpertInputGradArgs& a, int num_cus, hipStream_t stream);
 hipError_t launch_expert_weight_grad(const ExpertWeightGradArgs& a, int num_cus, hipStream_t stream);
+// Both, of one layer.
+hipError_t launch_expert_gradients(const ExpertInputGradArgs& input, const ExpertWeightGradArgs& weight, int num_cus,
+                                   hipStream_t stream);
 // The weight gradient of the experts with at most kOuterRows rows, and of those alone (called by
 // launch_expert_weight_grad, whose matrix kernel then leaves them out).
 constexpr int kOuterRows = 16;

@@ -156,27 +156,27 @@ moe_status_t backward_impl(bool gated, const void* d_y, const void* pre, const v
         a.d_z = d_z;
         if (moe::launch_expert_act_grad(a, cus, s) != hipSuccess) return MOE_ERR_HIP;
     }
-    if (d_x != nullptr && max_rows > 0) {
-        moe::ExpertInputGradArgs a;
-        a.rows = rows;
-        a.m = m;
-        a.k = k;
-        a.d_z = dz;
-        a.w = w;
-        a.d_x = d_x;
-        if (moe::launch_expert_input_grad(a, cus, s) != hipSuccess) return MOE_ERR_HIP;
-    }
-    if (d_w != nullptr) {
-        moe::ExpertWeightGradArgs a;
-        a.rows = rows;
-        a.m = m;
-        a.k = k;
-        a.d_z = dz;
-        a.x = x;
-        a.d_w = d_w;
-        a.d_bias = d_bias;
-        if (moe::launch_expert_weight_grad(a, cus, s) != hipSuccess) return MOE_ERR_HIP;
-    }
+    const bool input = d_x != nullptr && max_rows > 0, weight = d_w != nullptr;
+    moe::ExpertInputGradArgs in;
+    in.rows = rows;
+    in.m = m;
+    in.k = k;
+    in.d_z = dz;
+    in.w = w;
+    in.d_x = d_x;
+    moe::ExpertWeightGradArgs wg;
+    wg.rows = rows;
+    wg.m = m;
+    wg.k = k;
+    wg.d_z = dz;
+    wg.x = x;
+    wg.d_w = d_w;
+    wg.d_bias = d_bias;
+    hipError_t err = hipSuccess;
+    if (input && weight) err = moe::launch_expert_gradients(in, wg, cus, s);
+    else if (input) err = moe::launch_expert_input_grad(in, cus, s);
+    else if (weight) err = moe::launch_expert_weight_grad(wg, cus, s);
+    if (err != hipSuccess) return MOE_ERR_HIP;
     if (d_bias != nullptr && d_w == nullptr) {
         moe::ExpertBiasGradArgs a;
         a.rows = rows;

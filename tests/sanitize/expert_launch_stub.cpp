@@ -32,6 +32,12 @@ hipError_t launch_expert_weight_grad(const ExpertWeightGradArgs& a, int cus, hip
     require(rows_ok(a.rows) && a.d_w != nullptr && cus > 0, "weight grad");
     return hipSuccess;
 }
+hipError_t launch_expert_gradients(const ExpertInputGradArgs& in, const ExpertWeightGradArgs& w, int cus,
+                                   hipStream_t s) {
+    require(in.d_z == w.d_z && in.m == w.m && in.k == w.k && in.rows.offsets == w.rows.offsets, "gradients");
+    launch_expert_input_grad(in, cus, s);
+    return launch_expert_weight_grad(w, cus, s);
+}
 hipError_t launch_expert_act_grad(const ExpertActGradArgs& a, int cus, hipStream_t) {
     require(rows_ok(a.rows) && a.d_y != nullptr && a.pre != nullptr && a.d_z != nullptr && cus > 0, "act grad");
     return hipSuccess;

@@ -194,6 +194,31 @@ def test_backward_outputs_one_at_a_time(hip_device):
             assert torch.equal(_bits(one), _bits(full[i])), name
 
 
+# Tile sizes of the input's and the weight's gradient: both small, large and
+# small, small and large, both large; a second launch for the remainders where the
+# input's gradient is the only one; an expert with few rows beside them
+@pytest.mark.parametrize("shape", [([90, 0, 110], 136, 72), ([4104], 72, 2312), ([120] * 15 + [1], 520, 2312),
+                                   ([700, 3, 1801, 2500], 2056, 2312), ([1024, 1025, 1134, 1023], 1032, 3960)], ids=_id)
+def test_gradients_together_and_alone(hip_device, shape):
+    """Both gradients in one call have the bits of each alone."""
+    counts, n, k = shape
+    dev = hip_device
+    _say("gradients together and alone %s" % _id(shape))
+    m, e = sum(counts), len(counts)
+    off, x = offsets(counts, dev), rows_of(counts, k, 1, dev)
+    w, d_y = randn((e, n, k), 2, dev, k**-0.5), rows_of(counts, n, 3, dev)
+    both = [poisoned((m + TAIL, k), BF16, dev), poisoned((e, n, k), BF16, dev)]
+    moe.moe_grouped_linear_backward_bf16(d_y, x, w, off, d_x=both[0], d_w=both[1])
+    torch.cuda.synchronize()
+    X.check_products(d_y, x, w, off, both[0], both[1])
+    assert_untouched(both[0][m:], "d_x behind the last expert")
+    for name, whole in zip(("d_x", "d_w"), both):
+        one = poisoned(tuple(whole.shape), BF16, dev)
+        moe.moe_grouped_linear_backward_bf16(d_y, x, w, off, **{name: one})
+        torch.cuda.synchronize()
+        assert torch.equal(_bits(one), _bits(whole)), name
+
+
 def test_no_rows_at_all(hip_device):
     """max_rows of 0: the forward writes nothing, the weights' gradients are zeros."""
     dev = hip_device
