@@ -34,6 +34,7 @@
 extern "C" {
 #endif
 
+/* At an infinite z an activation and its slope are their limits (0 or infinity; 0 or 1). */
 typedef enum moe_activation {
     MOE_ACT_NONE = 0,      /* act(z) = z */
     MOE_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0 */

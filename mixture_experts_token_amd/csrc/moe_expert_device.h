@@ -42,7 +42,8 @@ constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGeluTanh = 3;
 
 // 1 / (1 + exp(-t)) with the hardware's exp2 and reciprocal (each within about
 // one unit in the last place of fp32; results are rounded to bf16 afterwards).
-// exp overflows to infinity for very negative t, whose reciprocal is 0.
+// exp overflows to infinity for very negative t, whose reciprocal is 0 (as a
+// subnormal one, below 2^-126, may be).
 __device__ __forceinline__ float logistic(float t) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * t));
 }
@@ -50,19 +51,25 @@ __device__ __forceinline__ float logistic(float t) {
 constexpr float kGeluC2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 
+// z s for a logistic s that is 0 far below: minus infinity gives the limit, 0,
+// and not the NaN of its product with 0 (a NaN z has a NaN s).
+constexpr float kLargest = 3.402823466e38f;
+__device__ __forceinline__ float times_logistic(float z, float s) { return __builtin_fmaxf(z, -kLargest) * s; }
+
 // act(z).  GELU's tanh form is z s with s the logistic of 2 c (z + 0.044715 z^3),
 // since (1 + tanh(y)) / 2 is the logistic of 2 y.
 template <int kAct>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (kAct == kActRelu) return z > 0.0f ? z : (z != z ? z : 0.0f);
-    if constexpr (kAct == kActSilu) return z * logistic(z);
-    if constexpr (kAct == kActGeluTanh) return z * logistic(kGeluC2 * (z + kGeluCubic * z * z * z));
+    if constexpr (kAct == kActSilu) return times_logistic(z, logistic(z));
+    if constexpr (kAct == kActGeluTanh) return times_logistic(z, logistic(kGeluC2 * (z + kGeluCubic * z * z * z)));
     return z;
 }
 
 // act(z) and act'(z).  Beyond |z| = 30 GELU's slope is 0 or 1 in fp32, so its
 // inner derivative is taken at +-30 there (z^2 would overflow against a zero
-// factor); a NaN stays a NaN.
+// factor); SiLU's is s + z s (1 - s) with a finite z beside the factor that is 0
+// at either infinity.  A NaN stays a NaN.
 template <int kAct>
 __device__ __forceinline__ void act_value_slope(float z, float& value, float& slope) {
     if constexpr (kAct == kActRelu) {
@@ -70,12 +77,12 @@ __device__ __forceinline__ void act_value_slope(float z, float& value, float& sl
         slope = z > 0.0f ? 1.0f : 0.0f;
     } else if constexpr (kAct == kActSilu) {
         const float s = logistic(z);
-        value = z * s;
-        slope = s + value * (1.0f - s);
+        value = times_logistic(z, s);
+        slope = s + __builtin_fminf(value, kLargest) * (1.0f - s);
     } else if constexpr (kAct == kActGeluTanh) {
         const float t = __builtin_fabsf(z) > 30.0f ? __builtin_copysignf(30.0f, z) : z;
         const float s = logistic(kGeluC2 * (t + kGeluCubic * t * t * t));
-        value = z * s;
+        value = times_logistic(z, s);
         slope = s + t * s * (1.0f - s) * kGeluC2 * (1.0f + 3.0f * kGeluCubic * t * t);
     } else {
         value = z;
