@@ -8,6 +8,11 @@
 //
 //   * A workgroup takes one expert, up to kMaxX of its rows and 64 rows of its
 //     weight (32 gate rows and their 32 up rows); it keeps the x rows in LDS.
+//     Half of that LDS and twice the workgroups for up to a row per expert was
+//     no faster (registers keep two workgroups on a CU either way) and halves
+//     the x rows of long ones: 256 experts, n x k 2048 x 7168 gated, 256 rows
+//     1553 us, 1413 as it is; 7168 x 2048, 8 rows 42.2, 41.0; 128 experts, 2048 x
+//     768, 16 rows 14.1, 13.0.
 //   * A wave streams 8 of those weight rows front to back, two 1 KiB loads a
 //     batch and four batches in flight, and multiplies each vector with the x
 //     rows by bf16 dot products into fp32 sums per lane; at a row's end the 64
@@ -31,6 +36,8 @@ constexpr int kStreamThreads = 512, kStreamWaves = kStreamThreads / 64;
 constexpr int kMaxX = 8;        // x rows per item at most
 constexpr int kWaveRows = 8;    // weight rows per wave and item
 constexpr int kBatch = 2, kInFlight = 4;
+constexpr int kXLds = 64 * 1024;  // x rows in LDS: two workgroups per CU, as many as their registers leave room for
+constexpr int kPerCu = 2;
 
 struct StreamParams {
     const int64_t* off;
@@ -139,9 +146,9 @@ __device__ __forceinline__ int stream_rows(const WaveRows& rows, const u32x4* xs
     return result;
 }
 
-template <bool kGated, int kAct, int kLdsBytes>
+template <bool kGated, int kAct>
 __global__ __launch_bounds__(kStreamThreads, 4) void expert_stream_kernel(StreamParams p) {
-    __shared__ __attribute__((aligned(16))) u32x4 xs[kLdsBytes / 16];
+    __shared__ __attribute__((aligned(16))) u32x4 xs[kXLds / 16];
     __shared__ int64_t pre_s[kMaxExperts + 1];
     __shared__ int64_t part[kStreamWaves];
     constexpr int kWaveCols = kGated ? kWaveRows / 2 : kWaveRows;
@@ -207,20 +214,18 @@ __global__ __launch_bounds__(kStreamThreads, 4) void expert_stream_kernel(Stream
     }
 }
 
-template <bool kGated, int kAct, int kLdsBytes>
-hipError_t launch_stream(const StreamParams& p, int num_cus, int per_cu, hipStream_t stream) {
-    hipLaunchKernelGGL((expert_stream_kernel<kGated, kAct, kLdsBytes>), dim3((unsigned)(num_cus * per_cu)),
-                       dim3(kStreamThreads), 0, stream, p);
+template <bool kGated, int kAct>
+hipError_t launch_stream(const StreamParams& p, int num_cus, hipStream_t stream) {
+    hipLaunchKernelGGL((expert_stream_kernel<kGated, kAct>), dim3((unsigned)(num_cus * kPerCu)), dim3(kStreamThreads),
+                       0, stream, p);
     return hipGetLastError();
 }
 
-constexpr int kSmallLds = 32 * 1024, kLargeLds = 64 * 1024;
-
-// x rows of k elements that fit: 8, 4, 2 or 1 (stream_rows reads that many), else 0.
-int x_rows_in(int lds_bytes, int64_t k) {
+// x rows of k elements that fit in LDS: 8, 4, 2 or 1 (stream_rows reads that many), else 0.
+int x_rows_in_lds(int64_t k) {
     const int64_t row = (k / 8 + kBatch * 64 - 1) / (kBatch * 64) * (kBatch * 64) * 16;
     int rows = kMaxX;
-    while (rows > 0 && rows * row > lds_bytes) rows /= 2;
+    while (rows > 0 && rows * row > kXLds) rows /= 2;
     return rows;
 }
 
@@ -236,7 +241,7 @@ int x_rows_in(int lds_bytes, int64_t k) {
 //     4 734 / 623; 2048 x 768: 2 71 / 83, 3 88 / 86, 4 103 / 95.
 //   2 otherwise.  4096 x 14336 (two fit): 1 112 / 147, 2 157 / 147, 3 205 / 147.
 bool expert_stream_applies(const ExpertForwardArgs& a) {
-    const int x = x_rows_in(kLargeLds, a.k);
+    const int x = x_rows_in_lds(a.k);
     const int64_t rows_per_expert = x == kMaxX && a.k >= 1024 ? 6 : x >= 4 ? 3 : 2;
     return x >= 1 && a.rows.max_rows <= rows_per_expert * a.rows.num_experts;
 }
@@ -260,17 +265,11 @@ hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, int64_t
     p.residual = static_cast<const uint16_t*>(a.residual);
     p.pre = static_cast<uint16_t*>(a.pre);
     p.out = static_cast<uint16_t*>(a.y);
-    // A row per expert or fewer: two x rows an item, and twice the workgroups.
-    const bool small = a.rows.max_rows <= a.rows.num_experts && x_rows_in(kSmallLds, a.k) >= 2;
-    p.x_rows = x_rows_in(small ? kSmallLds : kLargeLds, a.k);
+    p.x_rows = x_rows_in_lds(a.k);
     p.most_rows = *most_rows = a.rows.max_rows <= 2 * (int64_t)a.rows.num_experts ? a.rows.max_rows : 4 * (int64_t)p.x_rows;
     return with_activation(a.activation, [&](auto act) {
         constexpr int kAct = decltype(act)::value;
-        if (a.gated)
-            return small ? launch_stream<true, kAct, kSmallLds>(p, num_cus, 4, stream)
-                         : launch_stream<true, kAct, kLargeLds>(p, num_cus, 2, stream);
-        return small ? launch_stream<false, kAct, kSmallLds>(p, num_cus, 4, stream)
-                     : launch_stream<false, kAct, kLargeLds>(p, num_cus, 2, stream);
+        return a.gated ? launch_stream<true, kAct>(p, num_cus, stream) : launch_stream<false, kAct>(p, num_cus, stream);
     });
 }
 
