@@ -29,7 +29,7 @@ SOURCES = ["moe_permute_wave.hip", "moe_permute_fused.hip", "moe_permute_coarse.
            "moe_expert_gemm.hip", "moe_expert_stream.hip", "moe_expert_outer.hip",
            "moe_expert_grad.hip", "moe_unpermute_backward.hip", "moe_experts_api.cpp"]
 HEADERS = ["moe_launch.h", "moe_plan.h", "moe_permute_device.h", "moe_gemm_device.h", "moe_expert_launch.h",
-           "moe_expert_device.h", "moe_expert_tile.h"]
+           "moe_expert_plan.h", "moe_expert_device.h", "moe_expert_tile.h"]
 PROBE_SOURCES = ["hbm_probe.hip"]  # streaming-ceiling kernels used by bench.py only
 
 HIPCC_FLAGS = [

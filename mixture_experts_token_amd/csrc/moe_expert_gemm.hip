@@ -463,9 +463,11 @@ GemmParams params_of(const ExpertRows& rows, int64_t m, int64_t k, const void* a
 
 hipError_t launch_expert_forward(const ExpertForwardArgs& a, int num_cus, hipStream_t stream) {
     GemmParams p = params_of(a.rows, a.gated ? 2 * a.n : a.n, a.k, a.x, a.w, a.y);
-    const bool streamed = expert_stream_applies(a);
+    const StreamPlan plan = plan_stream(a.rows.max_rows, a.rows.num_experts, a.k);
+    const bool streamed = plan.x_rows > 0;
     if (streamed) {
-        const hipError_t err = launch_expert_stream(a, num_cus, &p.skip_rows, stream);
+        p.skip_rows = plan.most_rows;
+        const hipError_t err = launch_expert_stream(a, plan, num_cus, stream);
         if (err != hipSuccess || a.rows.max_rows <= p.skip_rows) return err;  // no expert can have more
     }
     p.n = a.n;

@@ -5,6 +5,8 @@
 
 #include <cstdint>
 
+#include "moe_expert_plan.h"
+
 namespace moe {
 
 // What every expert-layer launch takes: the rows' offsets and the layer's sizes.
@@ -79,10 +81,8 @@ struct UnpermuteBackwardArgs {
 };
 
 hipError_t launch_expert_forward(const ExpertForwardArgs& a, int num_cus, hipStream_t stream);
-// The forward for experts with few rows each (called by launch_expert_forward where it applies); experts
-// with more than most_rows (out) rows are left to the tiled kernel.
-bool expert_stream_applies(const ExpertForwardArgs& a);
-hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, int64_t* most_rows, hipStream_t stream);
+// The forward of the experts with few rows each (called by launch_expert_forward where the plan says so).
+hipError_t launch_expert_stream(const ExpertForwardArgs& a, const StreamPlan& plan, int num_cus, hipStream_t stream);
 hipError_t launch_expert_input_grad(const ExpertInputGradArgs& a, int num_cus, hipStream_t stream);
 hipError_t launch_expert_weight_grad(const ExpertWeightGradArgs& a, int num_cus, hipStream_t stream);
 // Both, of one layer.

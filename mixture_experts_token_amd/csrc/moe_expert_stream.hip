@@ -33,11 +33,11 @@ namespace moe {
 namespace {
 
 constexpr int kStreamThreads = 512, kStreamWaves = kStreamThreads / 64;
-constexpr int kMaxX = 8;        // x rows per item at most
+constexpr int kMaxX = kStreamMostX;  // x rows per item at most
 constexpr int kWaveRows = 8;    // weight rows per wave and item
 constexpr int kBatch = 2, kInFlight = 4;
-constexpr int kXLds = 64 * 1024;  // x rows in LDS: two workgroups per CU, as many as their registers leave room for
-constexpr int kPerCu = 2;
+constexpr int kPerCu = 2;         // as many workgroups as their registers leave room for
+static_assert(kBatch * 64 == kStreamBatchVecs, "the plan pads x rows to whole batches");
 
 struct StreamParams {
     const int64_t* off;
@@ -148,7 +148,7 @@ __device__ __forceinline__ int stream_rows(const WaveRows& rows, const u32x4* xs
 
 template <bool kGated, int kAct>
 __global__ __launch_bounds__(kStreamThreads, 4) void expert_stream_kernel(StreamParams p) {
-    __shared__ __attribute__((aligned(16))) u32x4 xs[kXLds / 16];
+    __shared__ __attribute__((aligned(16))) u32x4 xs[kStreamXLds / 16];
     __shared__ int64_t pre_s[kMaxExperts + 1];
     __shared__ int64_t part[kStreamWaves];
     constexpr int kWaveCols = kGated ? kWaveRows / 2 : kWaveRows;
@@ -221,38 +221,9 @@ hipError_t launch_stream(const StreamParams& p, int num_cus, hipStream_t stream)
     return hipGetLastError();
 }
 
-// x rows of k elements that fit in LDS: 8, 4, 2 or 1 (stream_rows reads that many), else 0.
-int x_rows_in_lds(int64_t k) {
-    const int64_t row = (k / 8 + kBatch * 64 - 1) / (kBatch * 64) * (kBatch * 64) * 16;
-    int rows = kMaxX;
-    while (rows > 0 && rows * row > kXLds) rows /= 2;
-    return rows;
-}
-
 }  // namespace
 
-// Where this kernel beats the tiled ones (us at r rows per expert, this / tiled;
-// n x k of the layer): up to
-//   6 rows per expert where 8 x rows of at least 1024 fit.  14336 x 4096 gated, 8
-//     experts: r 2 215 / 281, 4 268 / 355, 6 336 / 355, 8 433 / 355; 768 x 2048
-//     gated, 128 experts: 4 137 / 179, 6 164 / 179, 8 211 / 179; 7168 x 2048, 64
-//     experts: 4 303 / 392, 6 363 / 392, 8 448 / 392.
-//   3 where 4 fit, or shorter rows.  2048 x 7168 gated: 2 493 / 595, 3 618 / 609,
-//     4 734 / 623; 2048 x 768: 2 71 / 83, 3 88 / 86, 4 103 / 95.
-//   2 otherwise.  4096 x 14336 (two fit): 1 112 / 147, 2 157 / 147, 3 205 / 147.
-bool expert_stream_applies(const ExpertForwardArgs& a) {
-    const int x = x_rows_in_lds(a.k);
-    const int64_t rows_per_expert = x == kMaxX && a.k >= 1024 ? 6 : x >= 4 ? 3 : 2;
-    return x >= 1 && a.rows.max_rows <= rows_per_expert * a.rows.num_experts;
-}
-
-// An expert of many rows would have its weights streamed once per x_rows of
-// them: past four times that the tiled kernel takes it (64 experts, 2048 x 4096
-// gated, rows 120, 50, 30, 20 and 40 times 3: 370 -> 292 us; its launch costs
-// 6 - 9 us where no expert has that many).  With up to two rows per expert on
-// average all are streamed: that is never more than one of four experts' weights
-// beside what evenly spread rows read.
-hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, int64_t* most_rows, hipStream_t stream) {
+hipError_t launch_expert_stream(const ExpertForwardArgs& a, const StreamPlan& plan, int num_cus, hipStream_t stream) {
     StreamParams p{};
     p.off = a.rows.offsets;
     p.num_experts = a.rows.num_experts;
@@ -265,8 +236,8 @@ hipError_t launch_expert_stream(const ExpertForwardArgs& a, int num_cus, int64_t
     p.residual = static_cast<const uint16_t*>(a.residual);
     p.pre = static_cast<uint16_t*>(a.pre);
     p.out = static_cast<uint16_t*>(a.y);
-    p.x_rows = x_rows_in_lds(a.k);
-    p.most_rows = *most_rows = a.rows.max_rows <= 2 * (int64_t)a.rows.num_experts ? a.rows.max_rows : 4 * (int64_t)p.x_rows;
+    p.x_rows = plan.x_rows;
+    p.most_rows = plan.most_rows;
     return with_activation(a.activation, [&](auto act) {
         constexpr int kAct = decltype(act)::value;
         return a.gated ? launch_stream<true, kAct>(p, num_cus, stream) : launch_stream<false, kAct>(p, num_cus, stream);
