@@ -129,9 +129,13 @@ hipError_t launch_expert_act_grad(const ExpertActGradArgs& a, int num_cus, hipSt
     const int64_t nv = a.n / 8;
     const int64_t most = (a.rows.max_rows * nv + kGradThreads - 1) / kGradThreads;
     const int64_t blocks = most < (int64_t)num_cus * 8 ? most : (int64_t)num_cus * 8;
+    if (!a.gated && a.activation == kActNone) return hipErrorInvalidValue;  // d_z is d_y: there is no pass
     return with_activation(a.activation, [&](auto act) {
         constexpr int kAct = decltype(act)::value;
-        auto* kernel = a.gated ? expert_act_grad_kernel<true, kAct> : expert_act_grad_kernel<false, kAct>;
+        auto* kernel = expert_act_grad_kernel<true, kAct>;
+        if constexpr (kAct != kActNone) {
+            if (!a.gated) kernel = expert_act_grad_kernel<false, kAct>;
+        }
         hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kGradThreads), 0, stream, a.rows.offsets,
                            a.rows.num_experts, a.rows.max_rows, nv, static_cast<const u32x4*>(a.d_y),
                            static_cast<const u32x4*>(a.pre), static_cast<u32x4*>(a.d_z));

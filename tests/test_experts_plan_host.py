@@ -6,10 +6,15 @@ routing, what is streamed must stay within bounds that the plan is made for:
   * an expert's weights are streamed at most kStreamPasses times, or else the
     passes past each expert's first are at most a quarter of the experts;
   * a plan that streams nothing says so.
+
+The library holds the variants that calls reach and no others.
 """
 
 import os
+import re
 import subprocess
+
+from mixture_experts_token_amd import binding
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "mixture_experts_token_amd", "csrc")
@@ -63,3 +68,12 @@ def test_streamed_passes_are_bounded_for_any_routing(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", CSRC, "-o", str(exe), str(src)], check=True)
     res = subprocess.run([str(exe)], capture_output=True, text=True)
     assert res.returncode == 0, res.stdout[-3000:]
+
+
+def test_every_variant_is_reached():
+    """Activations 0 .. 3 of the gated layer's slopes, 1 .. 3 of the linear layer's (without one there is no pass)."""
+    out = subprocess.run(["nm", "-C", binding.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    slopes = set(re.findall(r"__device_stub__expert_act_grad_kernel<(\w+), (\d)>", out))
+    assert slopes == {("true", str(a)) for a in range(4)} | {("false", str(a)) for a in range(1, 4)}
+    streams = set(re.findall(r"__device_stub__expert_stream_kernel<(\w+), (\d)>", out))
+    assert streams == {(g, str(a)) for g in ("true", "false") for a in range(4)}
