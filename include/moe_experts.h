@@ -110,7 +110,7 @@ moe_status_t moe_grouped_linear_bf16(const void *x, const void *w, const void *b
  *   x, w             as in the forward; x may be NULL without d_w, w without d_x
  *   d_x [max_rows, k], d_w [num_experts, n, k], d_bias [num_experts, n]: bf16 (out) or NULL;
  *                    d_w and d_bias are zeros for an expert without rows
- * At least one output must be given.
+ * At least one output must be given, unless max_rows is 0.
  */
 moe_status_t moe_grouped_linear_backward_bf16(const void *d_y, const void *pre_activation, const void *x,
                                               const void *w, const int64_t *expert_first_token_offset,
@@ -131,7 +131,7 @@ moe_status_t moe_grouped_linear_backward_bf16(const void *d_y, const void *pre_a
  *   d_expanded_output [N*topk, hidden_size] of `dtype` (out) or NULL; rows that no slot names are
  *                     not written
  *   d_topk_weights    [N, topk] float (out) or NULL
- * At least one output must be given.  An entry of -1 writes no row and its
+ * At least one output must be given, unless there are no tokens.  An entry of -1 writes no row and its
  * weight's gradient is 0.  Any other entry outside [0, N*topk) is detected on
  * the device: it writes no row and its weight's gradient is NaN.  Two slots
  * with the same entry (no permute writes that) leave one slot's row, whole

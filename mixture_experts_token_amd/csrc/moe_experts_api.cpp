@@ -123,7 +123,8 @@ moe_status_t backward_impl(bool gated, const void* d_y, const void* pre, const v
         if (d_w != nullptr && x == nullptr) return MOE_ERR_INVALID_ARG;
         if (d_x != nullptr && w == nullptr) return MOE_ERR_INVALID_ARG;
     }
-    if (!differentiates && d_x == nullptr && d_w == nullptr && d_bias == nullptr) return MOE_ERR_INVALID_ARG;
+    if (max_rows > 0 && !differentiates && d_x == nullptr && d_w == nullptr && d_bias == nullptr)
+        return MOE_ERR_INVALID_ARG;
     const Buffer outs[] = {
         {d_z, bf16_bytes(max_rows, m)},
         {d_x, bf16_bytes(max_rows, k)},
@@ -140,6 +141,7 @@ moe_status_t backward_impl(bool gated, const void* d_y, const void* pre, const v
     if (check_buffers(outs) != MOE_OK) return MOE_ERR_MISALIGNED;
     if (!aligned(d_y, 16) || !aligned(pre, 16) || !aligned(x, 16) || !aligned(w, 16)) return MOE_ERR_MISALIGNED;
     if (any_overlap(outs, ins)) return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0 && d_w == nullptr && d_bias == nullptr) return MOE_OK;  // d_x and d_z of no rows
     int cus = 0;
     if (!cu_count(&cus)) return MOE_ERR_HIP;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -236,8 +238,8 @@ moe_status_t moe_unpermute_backward(const void* d_output, const void* expanded_o
     if (hidden_size < 1 || hidden_size > kMaxRowBytes / eb) return MOE_ERR_INVALID_ARG;
     const int64_t row_bytes = hidden_size * eb;
     if (row_bytes % 16 != 0) return MOE_ERR_MISALIGNED;
-    if (d_expanded_output == nullptr && d_topk_weights == nullptr) return MOE_ERR_INVALID_ARG;
     if (num_tokens == 0) return MOE_OK;
+    if (d_expanded_output == nullptr && d_topk_weights == nullptr) return MOE_ERR_INVALID_ARG;
     if (d_output == nullptr || inv_permuted_idx == nullptr) return MOE_ERR_INVALID_ARG;
     if (d_topk_weights != nullptr && expanded_output == nullptr) return MOE_ERR_INVALID_ARG;
     if (d_expanded_output != nullptr && topk_weights == nullptr) return MOE_ERR_INVALID_ARG;

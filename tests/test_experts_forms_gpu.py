@@ -113,6 +113,30 @@ def test_buffers_larger_than_the_rows(hip_device, case):
         assert_untouched(t[m:], name + " behind the last expert")
 
 
+def test_empty_batches(hip_device):
+    """Tensors of no rows have no address; every call takes them."""
+    dev, n, k = hip_device, 48, 64
+    off = offsets([0, 0], dev)
+    w, wg = randn((2, n, k), 1, dev), randn((2, 2 * n, k), 2, dev)
+
+    def rows(cols, dtype=BF16):
+        return torch.empty(0, cols, dtype=dtype, device=dev)
+
+    moe.moe_grouped_gated_gemm_bf16(rows(k), wg, off, rows(n), gate_up=rows(2 * n))
+    moe.moe_grouped_linear_bf16(rows(k), w, off, rows(n), residual=rows(n), pre_activation=rows(n), activation="silu")
+    moe.moe_grouped_linear_backward_bf16(rows(n), None, w, off, d_x=rows(k))
+    moe.moe_grouped_gated_gemm_backward_bf16(rows(n), rows(2 * n), None, wg, off, rows(2 * n), d_x=rows(k))
+    d_wg, d_b = poisoned((2, 2 * n, k), BF16, dev), poisoned((2, n), BF16, dev)
+    moe.moe_grouped_gated_gemm_backward_bf16(rows(n), rows(2 * n), rows(k), wg, off, rows(2 * n), d_x=rows(k), d_w=d_wg)
+    moe.moe_grouped_linear_backward_bf16(rows(n), None, w, off, d_bias=d_b, pre_activation=rows(n),
+                                         d_pre_activation=rows(n), activation="silu")
+    moe.moe_unpermute_backward(rows(k), rows(k), rows(2, torch.float32),
+                               torch.empty(0, dtype=torch.int32, device=dev), d_expanded_output=rows(k),
+                               d_topk_weights=rows(2, torch.float32))
+    torch.cuda.synchronize()
+    assert not d_wg.any() and not d_b.any()
+
+
 @pytest.mark.parametrize("rank", [0, 3])
 def test_block_of_one_rank(hip_device, rank):
     """moe_permute_local, both layers, moe_unpermute_local and back, as one of four expert-parallel ranks."""
