@@ -85,6 +85,15 @@ moe_status_t moe_grouped_gated_gemm_backward_bf16(const void *d_h, const void *g
  * moe_grouped_linear_bf16 -- one linear layer per expert with its epilogue:
  *     z[j][c] = sum_i x[j][i] * w[e][c][i] + bias[e][c]
  *     y[j][c] = act(z[j][c]) + residual[j][c]
+ * Without bias, activation and residual this is moe_grouped_gemm_bf16's product
+ * in other kernels (the sums' order differs, so single bits may).  That call
+ * takes n in multiples of 128 and k of 64 only.  Where both apply, this one is
+ * the faster from 128 rows per expert on (3 - 10 %) and with rows of 14336 (10 -
+ * 31 %), that one mostly at 4 to 64 rows of up to 7168 (by up to 14 %).  us, this
+ * / that, n x k: 4096 x 14336, 8 experts, 8192 rows 901 / 1000, 128 rows 164 /
+ * 238; 28672 x 4096, 8192 rows 1711 / 1827; 2048 x 768, 128 experts, 32768 rows
+ * 167 / 184, 2048 rows 99 / 86; 4096 x 7168, 256 experts, 32768 rows 3082 / 3408,
+ * 8192 rows 2613 / 2465.
  *
  *   x              [max_rows, k] bf16      w [num_experts, n, k] bf16
  *   bias           [num_experts, n] bf16 or NULL

@@ -279,6 +279,9 @@ moe_status_t moe_permute_quant_fp8(const void *hidden_states, int32_t dtype, con
  * Offsets that are not a valid prefix (off[0] != 0, a decreasing entry, the
  * -1 the permute writes for a rejected id, or off[E] > max_rows) are detected
  * on the device: nothing is written.  Needs no workspace.
+ * moe_grouped_linear_bf16 (moe_experts.h) takes every n and k in multiples of
+ * 8, bias, activation and residual; its comment says which is the faster where
+ * both apply.
  */
 moe_status_t moe_grouped_gemm_bf16(const void *x, const void *w, const int64_t *expert_first_token_offset,
                                    int32_t num_experts, int64_t max_rows, int64_t n, int64_t k, void *y,
