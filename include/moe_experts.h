@@ -112,7 +112,10 @@ moe_status_t moe_grouped_linear_bf16(const void *x, const void *w, const void *b
  *     d_z[j][c]    = d_y[j][c] * act'(pre_activation[j][c])     (d_y without an activation)
  *     d_x[j][i]    = sum_c d_z[j][c] * w[e][c][i]
  *     d_w[e][c][i] = sum_j d_z[j][c] * x[j][i]      d_bias[e][c] = sum_j d_z[j][c]
- * With an activation the sums take the bf16 d_z (see the gated backward).
+ * With an activation the products take the bf16 d_z (see the gated backward), and so
+ * does d_bias: it is the sum of the d_z that is returned, and is formed beside the
+ * weights' product from the operand at hand, without another pass over d_y and
+ * pre_activation.
  *
  *   pre_activation   [max_rows, n] bf16 as the forward wrote it; NULL exactly for MOE_ACT_NONE
  *   d_pre_activation [max_rows, n] bf16 (out): d_z; NULL exactly for MOE_ACT_NONE

@@ -283,7 +283,8 @@ struct TileSums {
 };
 
 // v plus the sum of a fragment's eight bf16 (dot products with ones: they run on
-// the vector units while the matrix cores work).
+// the vector units while the matrix cores work).  The bias gradient: summed in
+// fp32, from d_z as it was rounded to be this operand and returned.
 __device__ __forceinline__ float sum8(bf16x8 frag, float v) {
     const u32x4 w = __builtin_bit_cast(u32x4, frag);
     const uint32_t ones = 0x3F803F80u;

@@ -113,6 +113,32 @@ def test_buffers_larger_than_the_rows(hip_device, case):
         assert_untouched(t[m:], name + " behind the last expert")
 
 
+def test_layers_on_scratch_buffers(hip_device):
+    """MoEPermuteScratch made for more tokens than a call has: its views go to the layers as they are."""
+    dev, n, topk, e, hidden, width = hip_device, 21, 2, 5, 136, 72
+    scratch = moe.MoEPermuteScratch(64, topk, e, dev, hidden_size=hidden, hidden_dtype=BF16)
+    x, wts = randn((n, hidden), 1, dev), torch.full((n, topk), 0.5, device=dev)
+    ids = torch.stack([torch.arange(n) % e, (torch.arange(n) + 2) % e], 1).int().to(dev)
+    res = scratch.permute(x, ids)
+    xp, off, inv = res["permuted_hidden_states"], res["expert_first_token_offset"], res["inv_permuted_idx"]
+    w13, w2 = randn((e, 2 * width, hidden), 2, dev, hidden**-0.5), randn((e, hidden, width), 3, dev, width**-0.5)
+    rows = n * topk
+    h, y, out = poisoned((rows, width), BF16, dev), poisoned((rows, hidden), BF16, dev), poisoned((n, hidden), BF16, dev)
+    moe.moe_grouped_gated_gemm_bf16(xp, w13, off, h)
+    moe.moe_grouped_linear_bf16(h, w2, off, y)
+    moe.moe_unpermute(y, wts, inv, out)
+    d_y, d_w2 = poisoned((rows, hidden), BF16, dev), poisoned((e, hidden, width), BF16, dev)
+    moe.moe_unpermute_backward(out, y, wts, inv, d_expanded_output=d_y)
+    moe.moe_grouped_linear_backward_bf16(d_y, h, w2, off, d_w=d_w2)
+    torch.cuda.synchronize()
+    X.check_gated(xp, w13, off, "silu", h, None)
+    X.check_linear(h, w2, None, None, off, "none", y, None)
+    X.check_products(d_y, h, w2, off, None, d_w2)
+    slots = X.f64(y)[inv.long().cpu()].view(n, topk, hidden)
+    ref = 0.5 * slots.sum(1)
+    X.assert_within(out, ref, X.HALF * ref.abs() + X.accumulate(topk) * slots.abs().sum(1), "out")
+
+
 def test_empty_batches(hip_device):
     """Tensors of no rows have no address; every call takes them."""
     dev, n, k = hip_device, 48, 64
