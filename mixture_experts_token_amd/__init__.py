@@ -27,3 +27,12 @@ from .experts import (  # noqa: F401
     moe_grouped_linear_bf16,
     moe_unpermute_backward,
 )
+from .experts_8bit import (  # noqa: F401
+    moe_grouped_gated_gemm_fp8,
+    moe_grouped_gated_gemm_int8,
+    moe_grouped_linear_fp8,
+    moe_grouped_linear_int8,
+    moe_permute_quant_int8,
+    moe_quantize_rows_fp8,
+    moe_quantize_rows_int8,
+)

@@ -9,39 +9,12 @@
 
 #include <cstdint>
 
+#include "moe_api_checks.h"
 #include "moe_expert_launch.h"
 
+using namespace moe::api;
+
 namespace {
-
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;  // int32 row indices
-// Row lengths: a tile's 256 rows (512 of the gate-and-up pair) of 2^20
-// elements are addressed with 32-bit byte offsets.
-constexpr int64_t kMaxCols = int64_t(1) << 20;
-constexpr int64_t kMaxRowBytes = int64_t(1) << 40;
-
-bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-struct Buffer {
-    const void* p;
-    uint64_t bytes;
-};
-
-bool overlap(const Buffer& a, const Buffer& b) {
-    if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-template <int NO, int NI>
-bool any_overlap(const Buffer (&outs)[NO], const Buffer (&ins)[NI]) {
-    for (int i = 0; i < NO; ++i) {
-        for (int j = i + 1; j < NO; ++j)
-            if (overlap(outs[i], outs[j])) return true;
-        for (int j = 0; j < NI; ++j)
-            if (overlap(outs[i], ins[j])) return true;
-    }
-    return false;
-}
 
 // The checks every expert layer shares: sizes, activation, offsets.
 moe_status_t check_layer(const int64_t* off, int32_t num_experts, int64_t max_rows, int64_t n, int64_t k,
@@ -54,23 +27,6 @@ moe_status_t check_layer(const int64_t* off, int32_t num_experts, int64_t max_ro
     if (n % 8 != 0 || k % 8 != 0 || !aligned(off, 8)) return MOE_ERR_MISALIGNED;
     return MOE_OK;
 }
-
-template <int N>
-moe_status_t check_buffers(const Buffer (&all)[N]) {
-    for (const Buffer& b : all)
-        if (!aligned(b.p, 16)) return MOE_ERR_MISALIGNED;
-    return MOE_OK;
-}
-
-uint64_t bf16_bytes(int64_t a, int64_t b) { return 2ull * (uint64_t)a * (uint64_t)b; }
-
-bool cu_count(int* cus) {
-    int device = 0;
-    return hipGetDevice(&device) == hipSuccess &&
-           hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, device) == hipSuccess && *cus >= 1;
-}
-
-moe_status_t status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 moe_status_t forward_impl(bool gated, const void* x, const void* w, const void* bias, const void* residual,
                           const int64_t* off, int32_t num_experts, int64_t max_rows, int64_t n, int64_t k,

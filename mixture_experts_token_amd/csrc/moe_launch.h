@@ -47,7 +47,8 @@ struct QuantArgs {
     int32_t topk;
     int32_t group_vecs;             // 16-byte input vectors per scale group; 0: one scale per token
     bool all_local;                 // no expert map: every token has topk destinations
-    uint8_t* permuted_codes;        // [N*topk, H] E4M3FN
+    bool int8;                      // int8 codes (one scale per token), else E4M3FN
+    uint8_t* permuted_codes;        // [N*topk, H]
     float* permuted_scale;          // [N*topk, groups]
 };
 
@@ -70,6 +71,10 @@ hipError_t launch_quant_scatter(const QuantArgs& a, bool bf16, hipStream_t strea
 // Decode sizes (the wave plan, no expert map): index permute and quantise-scatter in one kernel.
 hipError_t launch_quant_permute_wave(const PermuteArgs& a, const QuantArgs& q, const PermutePlan& p, bool bf16,
                                      hipStream_t stream);
+// Both with int8 codes (called by the two above).
+hipError_t launch_quant_scatter_int8(const QuantArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_quant_permute_wave_int8(const PermuteArgs& a, const QuantArgs& q, const PermutePlan& p, bool bf16,
+                                          hipStream_t stream);
 hipError_t launch_permute(const PermuteArgs& a, const PermutePlan& p, void* workspace, hipStream_t stream);
 // Device address of the current device's static workspace (kStaticScratchBytes).
 hipError_t static_scratch_address(void** ptr);

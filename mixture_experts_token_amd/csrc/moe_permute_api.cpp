@@ -6,6 +6,7 @@
 // moe_permute_supported and the grouped GEMM, and (after every check of a
 // moe_permute_static_scratch call) the lookup of the static workspace.
 
+#include "moe_experts_8bit.h"
 #include "moe_permute.h"
 
 #include <hip/hip_runtime.h>
@@ -205,54 +206,13 @@ moe_status_t permute_impl(const void* hidden_states, int32_t dtype, const float*
     return moe::launch_permute(a, plan, workspace, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
-}  // namespace
-
-extern "C" {
-
-moe_status_t moe_permute(const void* hidden_states, int32_t dtype, const float* token_scale, const void* topk_ids,
-                         int32_t topk_ids_dtype, int64_t num_tokens, int64_t hidden_size, int32_t topk,
-                         int32_t num_experts, void* permuted_hidden_states, float* permuted_scale,
-                         int64_t* expert_first_token_offset, int32_t* permuted_idx, int32_t* inv_permuted_idx,
-                         void* workspace, size_t workspace_bytes, void* stream) {
-    return permute_impl(hidden_states, dtype, token_scale, topk_ids, topk_ids_dtype, num_tokens, hidden_size, topk,
-                        num_experts, nullptr, 0, permuted_hidden_states, permuted_scale, expert_first_token_offset,
-                        permuted_idx, inv_permuted_idx, workspace, workspace_bytes, stream);
-}
-
-moe_status_t moe_permute_static_scratch(const void* hidden_states, int32_t dtype, const float* token_scale,
-                                        const void* topk_ids, int32_t topk_ids_dtype, int64_t num_tokens,
-                                        int64_t hidden_size, int32_t topk, int32_t num_experts,
-                                        void* permuted_hidden_states, float* permuted_scale,
-                                        int64_t* expert_first_token_offset, int32_t* permuted_idx,
-                                        int32_t* inv_permuted_idx, void* stream) {
-    // moe_permute's checks and plan; the workspace is the device's static
-    // array (no allocation: it exists from library load).
-    return permute_impl(hidden_states, dtype, token_scale, topk_ids, topk_ids_dtype, num_tokens, hidden_size, topk,
-                        num_experts, nullptr, 0, permuted_hidden_states, permuted_scale, expert_first_token_offset,
-                        permuted_idx, inv_permuted_idx, nullptr, 0, stream, true);
-}
-
-moe_status_t moe_permute_local(const void* hidden_states, int32_t dtype, const float* token_scale,
-                               const void* topk_ids, int32_t topk_ids_dtype, int64_t num_tokens,
-                               int64_t hidden_size, int32_t topk, int32_t num_experts, const int32_t* expert_map,
-                               int32_t num_local_experts,
-                               void* permuted_hidden_states, float* permuted_scale,
-                               int64_t* expert_first_token_offset, int32_t* permuted_idx,
-                               int32_t* inv_permuted_idx, void* workspace, size_t workspace_bytes, void* stream) {
-    if (expert_map == nullptr) return MOE_ERR_INVALID_ARG;
-    return permute_impl(hidden_states, dtype, token_scale, topk_ids, topk_ids_dtype, num_tokens, hidden_size, topk,
-                        num_experts, expert_map, num_local_experts, permuted_hidden_states, permuted_scale,
-                        expert_first_token_offset, permuted_idx, inv_permuted_idx, workspace, workspace_bytes,
-                        stream);
-}
-
-moe_status_t moe_permute_quant_fp8(const void* hidden_states, int32_t dtype, const void* topk_ids,
-                                   int32_t topk_ids_dtype, int64_t num_tokens, int64_t hidden_size, int32_t topk,
-                                   int32_t num_experts, const int32_t* expert_map, int32_t num_local_experts,
-                                   int64_t group_size, uint8_t* permuted_codes, float* permuted_scale,
-                                   int64_t* expert_first_token_offset, int32_t* permuted_idx,
-                                   int32_t* inv_permuted_idx, void* workspace, size_t workspace_bytes,
-                                   void* stream) {
+// The quantising permutes; group_size 0 with int8 codes.
+moe_status_t quant_impl(bool int8, const void* hidden_states, int32_t dtype, const void* topk_ids,
+                        int32_t topk_ids_dtype, int64_t num_tokens, int64_t hidden_size, int32_t topk,
+                        int32_t num_experts, const int32_t* expert_map, int32_t num_local_experts,
+                        int64_t group_size, uint8_t* permuted_codes, float* permuted_scale,
+                        int64_t* expert_first_token_offset, int32_t* permuted_idx, int32_t* inv_permuted_idx,
+                        void* workspace, size_t workspace_bytes, void* stream) {
     // Quantiser checks first; permute_impl then checks the rest before it
     // enqueues anything, so a rejected call has no side effect.
     if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32) return MOE_ERR_UNSUPPORTED;
@@ -301,6 +261,7 @@ moe_status_t moe_permute_quant_fp8(const void* hidden_states, int32_t dtype, con
     q.topk = topk;
     q.group_vecs = group_size == 0 ? 0 : (int32_t)(group_size / epv);
     q.all_local = expert_map == nullptr;
+    q.int8 = int8;
     q.permuted_codes = permuted_codes;
     q.permuted_scale = permuted_scale;
     bool fused = false;
@@ -312,6 +273,72 @@ moe_status_t moe_permute_quant_fp8(const void* hidden_states, int32_t dtype, con
     return moe::launch_quant_scatter(q, dtype == MOE_DTYPE_BF16, static_cast<hipStream_t>(stream)) == hipSuccess
                ? MOE_OK
                : MOE_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_permute(const void* hidden_states, int32_t dtype, const float* token_scale, const void* topk_ids,
+                         int32_t topk_ids_dtype, int64_t num_tokens, int64_t hidden_size, int32_t topk,
+                         int32_t num_experts, void* permuted_hidden_states, float* permuted_scale,
+                         int64_t* expert_first_token_offset, int32_t* permuted_idx, int32_t* inv_permuted_idx,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+    return permute_impl(hidden_states, dtype, token_scale, topk_ids, topk_ids_dtype, num_tokens, hidden_size, topk,
+                        num_experts, nullptr, 0, permuted_hidden_states, permuted_scale, expert_first_token_offset,
+                        permuted_idx, inv_permuted_idx, workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_permute_static_scratch(const void* hidden_states, int32_t dtype, const float* token_scale,
+                                        const void* topk_ids, int32_t topk_ids_dtype, int64_t num_tokens,
+                                        int64_t hidden_size, int32_t topk, int32_t num_experts,
+                                        void* permuted_hidden_states, float* permuted_scale,
+                                        int64_t* expert_first_token_offset, int32_t* permuted_idx,
+                                        int32_t* inv_permuted_idx, void* stream) {
+    // moe_permute's checks and plan; the workspace is the device's static
+    // array (no allocation: it exists from library load).
+    return permute_impl(hidden_states, dtype, token_scale, topk_ids, topk_ids_dtype, num_tokens, hidden_size, topk,
+                        num_experts, nullptr, 0, permuted_hidden_states, permuted_scale, expert_first_token_offset,
+                        permuted_idx, inv_permuted_idx, nullptr, 0, stream, true);
+}
+
+moe_status_t moe_permute_local(const void* hidden_states, int32_t dtype, const float* token_scale,
+                               const void* topk_ids, int32_t topk_ids_dtype, int64_t num_tokens,
+                               int64_t hidden_size, int32_t topk, int32_t num_experts, const int32_t* expert_map,
+                               int32_t num_local_experts,
+                               void* permuted_hidden_states, float* permuted_scale,
+                               int64_t* expert_first_token_offset, int32_t* permuted_idx,
+                               int32_t* inv_permuted_idx, void* workspace, size_t workspace_bytes, void* stream) {
+    if (expert_map == nullptr) return MOE_ERR_INVALID_ARG;
+    return permute_impl(hidden_states, dtype, token_scale, topk_ids, topk_ids_dtype, num_tokens, hidden_size, topk,
+                        num_experts, expert_map, num_local_experts, permuted_hidden_states, permuted_scale,
+                        expert_first_token_offset, permuted_idx, inv_permuted_idx, workspace, workspace_bytes,
+                        stream);
+}
+
+moe_status_t moe_permute_quant_fp8(const void* hidden_states, int32_t dtype, const void* topk_ids,
+                                   int32_t topk_ids_dtype, int64_t num_tokens, int64_t hidden_size, int32_t topk,
+                                   int32_t num_experts, const int32_t* expert_map, int32_t num_local_experts,
+                                   int64_t group_size, uint8_t* permuted_codes, float* permuted_scale,
+                                   int64_t* expert_first_token_offset, int32_t* permuted_idx,
+                                   int32_t* inv_permuted_idx, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    return quant_impl(false, hidden_states, dtype, topk_ids, topk_ids_dtype, num_tokens, hidden_size, topk,
+                      num_experts, expert_map, num_local_experts, group_size, permuted_codes, permuted_scale,
+                      expert_first_token_offset, permuted_idx, inv_permuted_idx, workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_permute_quant_int8(const void* hidden_states, int32_t dtype, const void* topk_ids,
+                                    int32_t topk_ids_dtype, int64_t num_tokens, int64_t hidden_size, int32_t topk,
+                                    int32_t num_experts, const int32_t* expert_map, int32_t num_local_experts,
+                                    int8_t* permuted_codes, float* permuted_scale,
+                                    int64_t* expert_first_token_offset, int32_t* permuted_idx,
+                                    int32_t* inv_permuted_idx, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+    return quant_impl(true, hidden_states, dtype, topk_ids, topk_ids_dtype, num_tokens, hidden_size, topk,
+                      num_experts, expert_map, num_local_experts, 0, reinterpret_cast<uint8_t*>(permuted_codes),
+                      permuted_scale, expert_first_token_offset, permuted_idx, inv_permuted_idx, workspace,
+                      workspace_bytes, stream);
 }
 
 moe_status_t moe_grouped_gemm_bf16(const void* x, const void* w, const int64_t* expert_first_token_offset,

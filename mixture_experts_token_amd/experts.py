@@ -32,16 +32,21 @@ def _load() -> ctypes.CDLL:
     lib = binding.load_library()
     if _lib is not lib:
         p, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
-        lib.moe_grouped_gated_gemm_bf16.argtypes = [p, p, p, i32, i64, i64, i64, i32, p, p, p]
-        lib.moe_grouped_gated_gemm_backward_bf16.argtypes = [p, p, p, p, p, i32, i64, i64, i64, i32, p, p, p, p]
-        lib.moe_grouped_linear_bf16.argtypes = [p, p, p, p, p, i32, i64, i64, i64, i32, p, p, p]
-        lib.moe_grouped_linear_backward_bf16.argtypes = [p, p, p, p, p, i32, i64, i64, i64, i32, p, p, p, p, p]
-        lib.moe_unpermute_backward.argtypes = [p, p, i32, p, p, i64, i64, i32, p, p, p]
-        for fn in (lib.moe_grouped_gated_gemm_bf16, lib.moe_grouped_gated_gemm_backward_bf16,
-                   lib.moe_grouped_linear_bf16, lib.moe_grouped_linear_backward_bf16, lib.moe_unpermute_backward):
-            fn.restype = ctypes.c_int
+        _set_signatures(lib, {
+            "moe_grouped_gated_gemm_bf16": [p, p, p, i32, i64, i64, i64, i32, p, p, p],
+            "moe_grouped_gated_gemm_backward_bf16": [p, p, p, p, p, i32, i64, i64, i64, i32, p, p, p, p],
+            "moe_grouped_linear_bf16": [p, p, p, p, p, i32, i64, i64, i64, i32, p, p, p],
+            "moe_grouped_linear_backward_bf16": [p, p, p, p, p, i32, i64, i64, i64, i32, p, p, p, p, p],
+            "moe_unpermute_backward": [p, p, i32, p, p, i64, i64, i32, p, p, p],
+        })
         _lib = lib
     return lib
+
+
+def _set_signatures(lib, signatures) -> None:
+    for name, argtypes in signatures.items():
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = argtypes, ctypes.c_int
 
 
 def _activation(name) -> int:
@@ -77,7 +82,7 @@ def _buffer(t, name: str, dtypes, shape, device, optional: bool = False):
     return t.data_ptr()
 
 
-def _call(name: str, device, stream, args) -> None:
+def _call(name: str, device, stream, args, load=_load) -> None:
     """Calls the entry point on the tensors' device, whichever device is current."""
     import torch
 
@@ -86,10 +91,10 @@ def _call(name: str, device, stream, args) -> None:
         raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
     handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
     if torch._C._cuda_getDevice() == device.index:
-        status = getattr(_load(), name)(*args, handle)
+        status = getattr(load(), name)(*args, handle)
     else:
         with torch.cuda.device(device):
-            status = getattr(_load(), name)(*args, handle)
+            status = getattr(load(), name)(*args, handle)
     if status != MOE_OK:
         raise MoEError(status, name)
 
