@@ -28,10 +28,12 @@ SOURCES = ["moe_permute_wave.hip", "moe_permute_fused.hip", "moe_permute_coarse.
            "moe_permute_rows.hip", "moe_permute_launch.hip", "moe_unpermute.hip", "moe_quant_kernels.hip", "moe_gemm_kernels.hip", "moe_gemm_skinny.hip", "moe_permute_api.cpp",
            "moe_expert_gemm.hip", "moe_expert_stream.hip", "moe_expert_outer.hip",
            "moe_expert_grad.hip", "moe_unpermute_backward.hip", "moe_experts_api.cpp",
-           "moe_quant_int8.hip", "moe_quantize_rows.hip", "moe_expert_8bit.hip", "moe_experts_8bit_api.cpp"]
+           "moe_quant_int8.hip", "moe_quantize_rows.hip", "moe_expert_8bit.hip", "moe_expert_stream8.hip",
+           "moe_experts_8bit_api.cpp"]
 HEADERS = ["moe_launch.h", "moe_plan.h", "moe_permute_device.h", "moe_gemm_device.h", "moe_expert_launch.h",
            "moe_expert_plan.h", "moe_expert_device.h", "moe_expert_tile.h", "moe_expert_product.h",
-           "moe_quant_device.h", "moe_quant_kernel.h", "moe_expert_8bit_launch.h", "moe_api_checks.h"]
+           "moe_quant_device.h", "moe_quant_kernel.h", "moe_expert_8bit_launch.h",
+           "moe_expert_8bit_plan.h", "moe_api_checks.h"]
 PROBE_SOURCES = ["hbm_probe.hip"]  # streaming-ceiling kernels used by bench.py only
 
 HIPCC_FLAGS = [

@@ -31,8 +31,15 @@ hipError_t launch_expert_8bit(const Expert8BitArgs& a, int num_cus, hipStream_t 
     p.b_scale = a.w_scale;
     p.bias = static_cast<const uint16_t*>(a.bias);
     p.residual = static_cast<const uint16_t*>(a.residual);
-    const TileChoice tiles =
-        choose_tiles(a.rows.max_rows, most_groups(a.rows), a.n, a.gated ? 128 : 256, p.k, num_cus);
+    const Stream8Plan plan = plan_stream8(a.rows.max_rows, a.rows.num_experts, a.k);
+    const bool streamed = plan.groups > 0;
+    if (streamed) {
+        p.skip_rows = plan.most_rows;
+        const hipError_t err = launch_expert_stream8(a, plan, num_cus, stream);
+        if (err != hipSuccess || a.rows.max_rows <= p.skip_rows) return err;  // no expert can have more
+    }
+    TileChoice tiles = choose_tiles(a.rows.max_rows, most_groups(a.rows), a.n, a.gated ? 128 : 256, p.k, num_cus);
+    if (streamed) tiles = {true, false};
     p.apart = tiles.apart;
     return a.int8 ? launch_tiles<Operand::kInt8>(p, a, tiles, num_cus, stream)
                   : launch_tiles<Operand::kFp8>(p, a, tiles, num_cus, stream);

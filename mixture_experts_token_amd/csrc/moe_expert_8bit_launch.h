@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "moe_expert_8bit_plan.h"
 #include "moe_expert_launch.h"
 
 namespace moe {
@@ -34,6 +35,8 @@ struct Expert8BitArgs {
 };
 
 hipError_t launch_quantize_rows(const QuantizeRowsArgs& a, int num_cus, hipStream_t stream);
+// The experts with few rows each (called by launch_expert_8bit where the plan says so).
+hipError_t launch_expert_stream8(const Expert8BitArgs& a, const Stream8Plan& plan, int num_cus, hipStream_t stream);
 hipError_t launch_expert_8bit(const Expert8BitArgs& a, int num_cus, hipStream_t stream);
 
 }  // namespace moe
