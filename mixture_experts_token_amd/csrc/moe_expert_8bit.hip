@@ -31,7 +31,7 @@ hipError_t launch_expert_8bit(const Expert8BitArgs& a, int num_cus, hipStream_t 
     p.b_scale = a.w_scale;
     p.bias = static_cast<const uint16_t*>(a.bias);
     p.residual = static_cast<const uint16_t*>(a.residual);
-    const Stream8Plan plan = plan_stream8(a.rows.max_rows, a.rows.num_experts, a.k);
+    const Stream8Plan plan = plan_stream8(a.rows.max_rows, a.rows.num_experts, p.m, a.k, num_cus);
     const bool streamed = plan.groups > 0;
     if (streamed) {
         p.skip_rows = plan.most_rows;

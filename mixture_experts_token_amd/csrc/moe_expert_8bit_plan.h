@@ -11,6 +11,7 @@ namespace moe {
 constexpr int kStream8Waves = 8;
 constexpr int kStream8InFlight = 2;   // steps of loads ahead
 constexpr int kStream8Piece = 256;    // bytes of a row that a wave takes a step
+constexpr int kStream8WaveRows = 16;  // weight rows of a wave
 
 struct Stream8Plan {
     int groups;          // x rows per pass over an expert's weights, in fours (1, 2 or 4); 0: nothing is streamed
@@ -24,14 +25,19 @@ inline int stream8_steps(int64_t k, int kw) {
     return (int)((mine + kStream8InFlight - 1) / kStream8InFlight * kStream8InFlight);
 }
 
-inline Stream8Plan plan_stream8(int64_t max_rows, int64_t num_experts, int64_t k) {
+// cols: weight rows of an expert (n, or 2 n gated).
+inline Stream8Plan plan_stream8(int64_t max_rows, int64_t num_experts, int64_t cols, int64_t k, int num_cus) {
     Stream8Plan p = {0, 0, 0, 0};
     if (max_rows > 16 * num_experts) return p;
     p.groups = max_rows > 4 * num_experts ? 4 : max_rows > 2 * num_experts ? 2 : 1;
-    p.kw = kStream8Waves;
-    while (p.kw > 1 && stream8_steps(k, p.kw) < 4) p.kw /= 2;
-    p.steps = stream8_steps(k, p.kw);
     p.most_rows = 4 * 4 * p.groups;
+    const int64_t used = max_rows < num_experts ? max_rows : num_experts;
+    for (p.kw = kStream8Waves; p.kw > 1; p.kw /= 2) {
+        const int steps = stream8_steps(k, p.kw);
+        const int64_t rows = kStream8Waves / (p.kw / 2) * kStream8WaveRows;  // of an item with half as many
+        if (steps >= 8 || (steps >= 4 && used * ((cols + rows - 1) / rows) < 2 * num_cus)) break;
+    }
+    p.steps = stream8_steps(k, p.kw);
     return p;
 }
 

@@ -45,6 +45,7 @@ constexpr int kInFlight = kStream8InFlight;
 constexpr int kPiece = kStream8Piece;
 constexpr int kTiles = 4;                         // loads of 4 weight rows a step
 constexpr int kWaveRows = 4 * kTiles;
+static_assert(kWaveRows == kStream8WaveRows, "the plan counts items");
 // Workgroups per CU, as their registers leave room.
 template <int kGroups>
 constexpr int kPerCu = kGroups <= 2 ? 2 : 1;
@@ -68,10 +69,20 @@ struct Stream8Params {
 };
 
 struct Item {
-    int expert;
-    int64_t row0, c0;           // first x row, first output column
+    int expert, row0, c0;       // first x row, first output column
     int rows;                   // 0: no such item
 };
+
+// The expert of item `id`, the last e with pre[e] <= id: 64 lanes look at once
+// (a binary search is ten reads of LDS one after the other).
+__device__ __forceinline__ int expert_by_lanes(const int64_t* pre, int num_experts, int64_t id, int lane) {
+    const int span = (num_experts + 63) / 64;
+    int at = lane * span;
+    const int first = (__popcll(__ballot(at < num_experts && pre[at < num_experts ? at : 0] <= id)) - 1) * span;
+    if (span == 1) return first;
+    at = first + lane;
+    return first + __popcll(__ballot(lane < span && at < num_experts && pre[at < num_experts ? at : 0] <= id)) - 1;
+}
 
 template <Operand kOp>
 struct Sum4 {
@@ -124,8 +135,10 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<kGroups>) void expert_stream8_
     __shared__ T sums_s[2][kWaves][kGroups][64];
     __shared__ int64_t pre_s[kMaxExperts + 1];
     __shared__ int64_t part[kWaves];
+    __shared__ int off_s[kMaxExperts + 1];           // the offsets: a load from memory would wait for those in flight
+    for (int e = threadIdx.x; e <= p.num_experts; e += kThreads) off_s[e] = (int)p.off[e];
     const int cw = kWaves / p.kw, item_cols = cw * kWaveCols;
-    const int64_t blocks = (p.n + item_cols - 1) / item_cols;
+    const int blocks = (int)((p.n + item_cols - 1) / item_cols);
     const bool ok = expert_items<kThreads>(p.off, p.num_experts, p.max_rows, pre_s, part, [&](int64_t rows) {
         return rows > p.most_rows ? 0 : (rows + kRows - 1) / kRows * blocks;
     });
@@ -137,12 +150,18 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<kGroups>) void expert_stream8_
     auto item_of = [&](int64_t id) __attribute__((always_inline)) {
         Item it = {0, 0, 0, 0};
         if (id >= total) return it;
-        it.expert = expert_of_item(pre_s, p.num_experts, id);
-        const int64_t local = id - wave_uniform64(pre_s[it.expert]), group = local / blocks;
-        it.c0 = (local - group * blocks) * item_cols;
-        it.row0 = wave_uniform64(p.off[it.expert]) + group * kRows;
-        const int64_t left = wave_uniform64(p.off[it.expert + 1]) - it.row0;
-        it.rows = (int)(left < kRows ? left : kRows);
+        it.expert = __builtin_amdgcn_readfirstlane(expert_by_lanes(pre_s, p.num_experts, id, lane));
+        int64_t local = id - wave_uniform64(pre_s[it.expert]);
+        int group = 0;
+        if (local >= blocks) {  // few experts have more rows than one pass takes
+            const int64_t q = local / blocks;
+            group = (int)q;
+            local -= q * blocks;
+        }
+        it.c0 = (int)local * item_cols;
+        it.row0 = __builtin_amdgcn_readfirstlane(off_s[it.expert]) + group * kRows;
+        const int left = __builtin_amdgcn_readfirstlane(off_s[it.expert + 1]) - it.row0;
+        it.rows = left < kRows ? left : kRows;
         return it;
     };
 
@@ -155,13 +174,14 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<kGroups>) void expert_stream8_
         const char* base = p.w + ((int64_t)it.expert * (kGated ? 2 : 1) * p.n + (cols > 0 ? c : 0)) * p.k;
         rw[0] = resource(base, cols * p.k);
         rw[1] = kGated ? resource(base + p.n * p.k, cols * p.k) : rw[0];
-        rx = resource(p.x + it.row0 * p.k, cols > 0 ? (int64_t)it.rows * p.k : 0);
+        rx = resource(p.x + (int64_t)it.row0 * p.k, cols > 0 ? (int64_t)it.rows * p.k : 0);
     };
     const uint32_t row_off = (uint32_t)(lane % 16 / 4) * p.k, four_rows = 4u * p.k;
     const int lane_pos = lane / 16 * 64 + lane % 4 * 16;
+    const bool one_round = p.steps == kInFlight;     // the loads are a whole item ahead
+    const int64_t grid = gridDim.x;
+    Item it = item_of(blockIdx.x), next = item_of(blockIdx.x + grid), after = next;
     int load_step = 0;
-    int64_t load_id = blockIdx.x;
-    Item load_next;
     auto issue = [&](int d) __attribute__((always_inline)) {
         const int pos = (load_step * p.kw + wk) * kPiece + lane_pos;
         const uint32_t off = pos < p.k ? row_off + pos : kOutOfRange;
@@ -174,22 +194,37 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<kGroups>) void expert_stream8_
             xv[d][g] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(off + g * four_rows), 0, 0);
         if (++load_step == p.steps) {
             load_step = 0;
-            load_id += gridDim.x;
-            aim(load_next);
+            aim(one_round ? after : next);
         }
         // in this order: hoisted above the uses of the step before, the refills
         // would make the compiler wait for all of them
         __builtin_amdgcn_sched_barrier(0);
     };
-    aim(item_of(load_id));
-    load_next = item_of(load_id + gridDim.x);
+    aim(it);
 #pragma unroll
     for (int d = 0; d < kInFlight; ++d) issue(d);
 
     int buf = 0;
-    for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-        const Item it = item_of(id);
-        load_next = item_of(load_id + gridDim.x);
+    for (int64_t id = blockIdx.x; id < total; id += grid) {
+        after = item_of(id + 2 * grid);
+        // What this wave finishes of the item, up to kGroups times 64 outputs: group
+        // g of x rows, columns of the waves fc kw ..; their scales are loaded ahead of
+        // the item's loads, so that waiting for them is not waiting for those.
+        int64_t at[kGroups];
+        int row[kGroups];
+        bool mine[kGroups];
+        float xs[kGroups], wa[kGroups], wb[kGroups];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int q = wave + i * kWaves, fc = q / kGroups, t = lane % 4;
+            const int c = it.c0 + fc * kWaveCols + t * 4 + lane / 16;
+            row[i] = q % kGroups * 4 + lane % 16 / 4;
+            mine[i] = q < cw * kGroups && row[i] < it.rows && c < p.n && !(kGated && t >= kTiles / 2);
+            at[i] = (int64_t)it.expert * p.n + c;
+            xs[i] = mine[i] ? p.x_scale[it.row0 + row[i]] : 0.0f;
+            wa[i] = mine[i] ? p.w_scale[at[i] + (kGated ? it.expert * p.n : 0)] : 0.0f;
+            wb[i] = kGated && mine[i] ? p.w_scale[at[i] + (it.expert + 1) * p.n] : 0.0f;
+        }
         V acc[kTiles][kGroups] = {};
         for (int s = 0; s < p.steps; s += kInFlight) {
 #pragma unroll
@@ -217,31 +252,30 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<kGroups>) void expert_stream8_
         // every wave's sums are there; the loads in flight are not waited for.  The
         // next item's go to the other buffer, and no wave is two items ahead.
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        for (int q = wave; q < cw * kGroups; q += kWaves) {
-            const int fc = q / kGroups, g = q % kGroups, t = lane % 4;
-            const int row = g * 4 + lane % 16 / 4;
-            const int64_t c = it.c0 + fc * kWaveCols + t * 4 + lane / 16;
-            if (row >= it.rows || c >= p.n || (kGated && t >= kTiles / 2)) continue;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            if (!mine[i]) continue;
+            const int q = wave + i * kWaves, fc = q / kGroups, g = q % kGroups;
             T a = 0, b = 0;
-            for (int i = 0; i < p.kw; ++i) {
-                a += sums_s[buf][fc * p.kw + i][g][lane];
-                if constexpr (kGated) b += sums_s[buf][fc * p.kw + i][g][lane + kTiles / 2];
+            for (int w = fc * p.kw; w < (fc + 1) * p.kw; ++w) {
+                a += sums_s[buf][w][g][lane];
+                if constexpr (kGated) b += sums_s[buf][w][g][lane + kTiles / 2];
             }
-            const int64_t j = it.row0 + row, at = (int64_t)it.expert * p.n + c;
-            const float xs = p.x_scale[j];
+            const int64_t out = (int64_t)(it.row0 + row[i]) * p.n + (at[i] - (int64_t)it.expert * p.n);
             float y;
             if constexpr (kGated) {
-                const float* ws = p.w_scale + at + (int64_t)it.expert * p.n;
-                y = act_value<kAct>((float)a * ws[0] * xs) * ((float)b * ws[p.n] * xs);
+                y = act_value<kAct>((float)a * wa[i] * xs[i]) * ((float)b * wb[i] * xs[i]);
             } else {
-                float z = (float)a * p.w_scale[at] * xs;
-                if (p.bias != nullptr) z += bf16_to_float(p.bias[at]);
+                float z = (float)a * wa[i] * xs[i];
+                if (p.bias != nullptr) z += bf16_to_float(p.bias[at[i]]);
                 y = act_value<kAct>(z);
-                if (p.residual != nullptr) y += bf16_to_float(p.residual[j * p.n + c]);
+                if (p.residual != nullptr) y += bf16_to_float(p.residual[out]);
             }
-            p.out[j * p.n + c] = (uint16_t)pack_bf16(y, 0.0f);
+            p.out[out] = (uint16_t)pack_bf16(y, 0.0f);
         }
         buf ^= 1;
+        it = next;
+        next = after;
     }
 }
 
