@@ -1,36 +1,536 @@
-// moe_expert_8bit.hip -- the experts' layers on int8 and fp8 codes: the forward
-// products of moe_expert_product.h, with the codes loaded as half as many bf16.
+// moe_expert_8bit.hip -- the experts' layers on int8 and fp8 codes: grouped
+// products on tiles (gfx950 MFMA).
+//
+//   sum[j][c] = sum_T x[j][T] w[e][c][T]   over codes, then scales and epilogue
+//
+// The tiles, their order and the schedule of a step are those of the bf16
+// products (moe_expert_tile.h, moe_expert_tile_list.h): codes are loaded as half
+// as many bf16, so that a step is 128 codes of a row, at the same bytes and the
+// same matrix-core cycles (v_mfma_i32_32x32x32_i8, v_mfma_f32_32x32x64_f8f6f4).
+// A tile of so many rows and columns takes half as long, and what lies between
+// two tiles weighs twice as much.  So here
+//
+//   * loads do not stop at a tile's end: its last steps bring the next tile's
+//     first ones, and the two rows of waves stay one barrier apart throughout;
+//   * scales and bias come into LDS with a tile's first step, and everything that
+//     is read from LDS while loads into it are under way is read in inline asm
+//     (the compiler would wait for all of them).
 
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
 
 #include "moe_expert_8bit_launch.h"
-#include "moe_expert_product.h"
+#include "moe_expert_tile.h"
+#include "moe_expert_tile_list.h"
 
 namespace moe {
 
 namespace {
 
-template <Operand kOp>
-hipError_t launch_tiles(const GemmParams& p, const Expert8BitArgs& a, const TileChoice& tiles, int num_cus,
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+
+struct Product8Params {
+    const int64_t* off;
+    int num_experts;
+    int64_t max_rows;
+    int64_t m, k;              // w is [num_experts, m, 2 k]: k counts pairs of codes
+    int64_t n;                 // output columns (m, or m / 2 gated)
+    const uint16_t* x;
+    const uint16_t* w;
+    const float* x_scale;      // [max_rows]
+    const float* w_scale;      // [num_experts, m]
+    const uint16_t* bias;
+    const uint16_t* residual;
+    uint16_t* out;
+    bool apart;                // light remainders may go to a launch of small tiles (remainders_apart)
+    int64_t skip_rows;         // experts with up to that many rows are left out (-1: none)
+};
+
+constexpr int kColScale = 256, kUpScale = 128;   // places in a tile's scales: rows, columns, up columns
+struct Product8Lds {
+    char tiles[kTileLds];
+    char blocks[kTileThreads / 64 * kBlockBytes];
+    float scale[2][512];                         // of this tile and the next
+    uint32_t bias[2][128];
+    int pre[kMaxExperts + 1];                    // tiles of the experts before
+    int off[kMaxExperts + 1];
+};
+static_assert(sizeof(Product8Lds) <= 160 * 1024, "LDS of a CU");
+static_assert((kMaxExperts + 1) * 8 + kTileThreads / 8 <= kTileLds, "the tiles' LDS holds the lists first");
+
+// LDS reads that the compiler does not see.
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)p; }
+__device__ __forceinline__ int lds_int(const int* p) {
+    int v;
+    asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(v) : "v"(lds_address(p)) : "memory");
+    return v;
+}
+// A lane's four runs of four columns, 8 apart: scales, bias.
+__device__ __forceinline__ void lds_runs(const float* p, f32x4 (&v)[4]) {
+    asm volatile(
+        "ds_read_b128 %0, %4\n\t"
+        "ds_read_b128 %1, %4 offset:32\n\t"
+        "ds_read_b128 %2, %4 offset:64\n\t"
+        "ds_read_b128 %3, %4 offset:96\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(lds_address(p))
+        : "memory");
+}
+__device__ __forceinline__ void lds_runs(const uint32_t* p, u32x2 (&v)[4]) {
+    asm volatile(
+        "ds_read_b64 %0, %4\n\t"
+        "ds_read_b64 %1, %4 offset:16\n\t"
+        "ds_read_b64 %2, %4 offset:32\n\t"
+        "ds_read_b64 %3, %4 offset:48\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(lds_address(p))
+        : "memory");
+}
+
+// What the codes are, and the sums of their products: 32-bit integers (exact) or
+// fp32.
+enum class Codes8 { kInt8, kFp8 };
+template <Codes8 kCodes>
+struct Sum16 {
+    typedef f32x16 V;
+};
+template <>
+struct Sum16<Codes8::kInt8> {
+    typedef i32x16 V;
+};
+
+template <bool kSmall, Codes8 kCodes>
+struct TileSums8 {  // laid out as TileSums
+    typedef TileShape<kSmall> S;
+    typename Sum16<kCodes>::V v[S::kHalves][S::kBlocks][2];
+};
+
+// Two fragments of 16 codes as one of 32 (which of T a lane holds does not
+// matter, as long as both operands hold the same).
+__device__ __forceinline__ i32x8 join(bf16x8 lo, bf16x8 hi) {
+    return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// acc += a b over a step.
+template <Codes8 kCodes, int kBlocks>
+__device__ __forceinline__ void multiply8(const bf16x8 (&a)[kBlocks][4], const Frags& b,
+                                          typename Sum16<kCodes>::V (&acc)[kBlocks][2]) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int s = 0; s < 4; s += kCodes == Codes8::kInt8 ? 1 : 2)
+#pragma unroll
+        for (int f = 0; f < kBlocks; ++f)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if constexpr (kCodes == Codes8::kInt8)
+                    acc[f][c] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, b.v[c][s]),
+                                                                      __builtin_bit_cast(i32x4, a[f][s]), acc[f][c], 0,
+                                                                      0, 0);
+                else  // format 0 of both is E4M3; scales of 0 select the form without scales
+                    acc[f][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        join(b.v[c][s], b.v[c][s + 1]), join(a[f][s], a[f][s + 1]), acc[f][c], 0, 0, 0, 0, 0, 0);
+            }
+    __builtin_amdgcn_s_setprio(0);
+}
+
+struct Tile8 {
+    TileCoord t;
+    const char *a, *b;   // its first row of x and of this wave's rows of w
+    int rl, cl;          // rows and columns that exist; 0: no such tile
+};
+
+// The step of a tile that the loads are at: what is left of both operands, kept
+// from step to step (worked out anew, it took longer than the other waves'
+// products: 890 -> 1059 us for 8 experts of 1024 rows, 14336 x 4096 gated).
+struct Cursor8 {
+    const char *a, *b;
+    int a_bytes, b_bytes;  // from there to the end of the tile's rows
+    int left;              // 16-byte vectors of a row
+    int step;
+
+    __device__ __forceinline__ void aim(const Tile8& t, int row_bytes) {
+        a = t.a;
+        b = t.b;
+        a_bytes = t.rl * row_bytes;
+        b_bytes = t.cl * row_bytes;
+        left = t.rl > 0 ? row_bytes / 16 : 0;
+        step = 0;
+    }
+    // To the next step; after the last one to `next`.
+    __device__ __forceinline__ void advance(int steps, const Tile8& next, int row_bytes) {
+        a += kStepT * 2;
+        b += kStepT * 2;
+        a_bytes -= kStepT * 2;
+        b_bytes -= kStepT * 2;
+        left -= kStepT / 8;
+        if (++step == steps) aim(next, row_bytes);
+    }
+    // Past a row's end nothing is in range, and zeros are loaded.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const char* base, int bytes) const {
+        return __builtin_amdgcn_make_buffer_rsrc((void*)wave_uniform64((int64_t)base), 0,
+                                                 __builtin_amdgcn_readfirstlane(left > 0 ? bytes : 0), 0x00020000);
+    }
+};
+
+// A tile's loads.  The operands lie T-contiguous: offsets within a half tile are
+// the same for every tile.
+template <bool kGated, bool kOnceB>
+struct Loader8 {
+    char* lds;
+    uint32_t a_voff[2], b_voff[2];
+    uint32_t a_half, b_half;
+    int wave, lane;
+
+    __device__ __forceinline__ Loader8(char* lds_, int row_bytes) : lds(lds_) {
+        lane = opaque_lane();
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        const int b_row = kGated ? wave / 4 * 32 + wave % 2 * 16 : wave * 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            a_voff[i] = load_offset<true>(row_bytes, wave * 16, lane, i);
+            b_voff[i] = load_offset<true>(row_bytes, b_row, lane, i);
+        }
+        a_half = 128u * row_bytes;
+        b_half = (kGated ? 64u : 128u) * row_bytes;
+    }
+    __device__ __forceinline__ void a(char* dst, const Cursor8& c, uint32_t half) const {
+        load_half<true>(dst, c.resource(c.a, c.a_bytes), a_voff, half, c.left, wave, lane);
+    }
+    template <int kHalves>
+    __device__ __forceinline__ void b(char* dst, const Cursor8& c) const {
+        const __amdgpu_buffer_rsrc_t r = c.resource(c.b, c.b_bytes);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+            load_half<true, kOnceB>(dst + h * kHalfBytes, r, b_voff, h * b_half, c.left, wave, lane);
+    }
+    // Large tiles: B and A's first half (6 loads of a wave), A's second half (2).
+    __device__ __forceinline__ void b_a0(const Cursor8& c, uint32_t at) const {
+        char* stage = lds + (at % 2) * kStageBytes;
+        b<2>(stage + kPartB * kHalfBytes, c);
+        a(stage + kPartA * kHalfBytes, c, 0);
+    }
+    __device__ __forceinline__ void a1(const Cursor8& c, uint32_t at) const {
+        a(lds + (at % 2) * kStageBytes + (kPartA + 1) * kHalfBytes, c, a_half);
+    }
+    // Small ones: 4.
+    __device__ __forceinline__ void small(const Cursor8& c, uint32_t at) const {
+        char* stage = lds + (at % kSmallStages) * kSmallStageBytes;
+        b<1>(stage + kHalfBytes, c);
+        a(stage, c, 0);
+    }
+};
+
+// A block's sums as values: scales of the column and of the row.
+template <typename V>
+__device__ __forceinline__ f32x16 scaled(const V& sums, const f32x4 (&col)[4], float row) {
+    f32x16 v;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = (float)sums[i] * col[i / 4][i % 4] * row;
+    return v;
+}
+
+template <Codes8 kCodes, bool kGated, int kAct, bool kSmall, bool kOnceB>
+__global__ __launch_bounds__(kTileThreads, 1) void expert_product8_kernel(Product8Params p) {
+    typedef TileShape<kSmall> S;
+    constexpr int kColsPerTile = kGated ? S::kCols / 2 : S::kCols;
+    constexpr int kAhead = kSmall ? kSmallStages - 1 : 2;  // steps that loads run ahead
+    __shared__ __attribute__((aligned(1024))) Product8Lds mem;
+    const int64_t col_tiles = (p.n + kColsPerTile - 1) / kColsPerTile;
+    const int num_experts = p.num_experts;
+
+    // The list of tiles.
+    Part part = Part::kAll;
+    {
+        int64_t* const pre = reinterpret_cast<int64_t*>(mem.tiles);
+        int64_t* const sums = pre + kMaxExperts + 1;
+        if (p.apart) {
+            constexpr int kLargeCols = kGated ? 128 : 256;  // in large tiles, whichever this launch has
+            const int64_t large_cols = (p.n + kLargeCols - 1) / kLargeCols;
+            if (!expert_items<kTileThreads>(p.off, num_experts, p.max_rows, pre, sums,
+                                            [&](int64_t rows) { return light_remainder(rows) ? large_cols : 0; }))
+                return;
+            const int64_t light = pre[num_experts];
+            __syncthreads();
+            expert_items<kTileThreads>(p.off, num_experts, p.max_rows, pre, sums, [&](int64_t rows) {
+                return row_tiles<TileShape<false>::kRows>(rows, Part::kNoLight) * large_cols;
+            });
+            const int64_t heavy = pre[num_experts];
+            __syncthreads();
+            const bool apart = remainders_apart(heavy, light, p.k, gridDim.x);
+            if (kSmall && !apart) return;  // the launch before took them
+            if (apart) part = kSmall ? Part::kLight : Part::kNoLight;
+        }
+        if (!expert_items<kTileThreads>(p.off, num_experts, p.max_rows, pre, sums, [&](int64_t rows) {
+                return rows <= p.skip_rows ? (int64_t)0 : row_tiles<S::kRows>(rows, part) * col_tiles;
+            }))
+            return;
+        for (int e = threadIdx.x; e <= num_experts; e += kTileThreads) {
+            mem.pre[e] = (int)pre[e];  // fits: the host bounds rows times columns
+            mem.off[e] = (int)p.off[e];
+        }
+        __syncthreads();
+    }
+    const int total = __builtin_amdgcn_readfirstlane(mem.pre[num_experts]);
+    const int grid = gridDim.x;
+    const int slot = (int)(blockIdx.x % kXcdCount) * (grid / kXcdCount) + (int)(blockIdx.x / kXcdCount);  // a chunk per XCD
+    if (slot >= total) return;
+
+    const int row_bytes = (int)p.k * 2;
+    const Loader8<kGated, kOnceB> load(mem.tiles, row_bytes);
+    const int wave = load.wave;
+    auto tile_of = [&](int64_t id) __attribute__((always_inline)) {
+        Tile8 o{};
+        const bool up = kGated && wave % 4 >= 2;  // which rows of w this wave loads
+        o.a = reinterpret_cast<const char*>(p.x);
+        o.b = reinterpret_cast<const char*>(p.w);
+        if (id >= total) return o;
+        // the expert: the last e with pre[e] <= id, 64 lanes at once
+        const int span = (num_experts + 63) / 64;
+        auto count = [&](int at, bool in) __attribute__((always_inline)) {
+            const bool here = in && at < num_experts;
+            const int v = lds_int(mem.pre + (here ? at : 0));
+            return __popcll(__ballot(here && v <= (int)id)) - 1;
+        };
+        int e = count(load.lane * span, true) * span;
+        if (span > 1) e += count(e + load.lane, load.lane < span);
+        e = __builtin_amdgcn_readfirstlane(e);
+        o.t.expert = e;
+        o.t.first = __builtin_amdgcn_readfirstlane(lds_int(mem.off + e));
+        o.t.count = __builtin_amdgcn_readfirstlane(lds_int(mem.off + e + 1)) - o.t.first;
+        place_tile<false, S::kRows>(o.t, id - __builtin_amdgcn_readfirstlane(lds_int(mem.pre + e)), p.m, col_tiles,
+                                    kColsPerTile, part);
+        const int64_t rows_left = o.t.count - o.t.r0, cols_left = p.n - o.t.c0;
+        o.rl = (int)(rows_left < S::kRows ? rows_left : S::kRows);
+        o.cl = (int)(cols_left < kColsPerTile ? cols_left : kColsPerTile);
+        o.a = reinterpret_cast<const char*>(p.x + (o.t.first + o.t.r0) * p.k);
+        o.b = reinterpret_cast<const char*>(p.w + ((int64_t)e * p.m + (up ? p.n : 0) + o.t.c0) * p.k);
+        return o;
+    };
+    // A tile's scales and bias: one load of 256 bytes of each wave, two of the bias's.
+    auto load_scales = [&](const Tile8& c, int buf) __attribute__((always_inline)) {
+        const int i = wave % 4 * 64 + load.lane;
+        const int64_t at = (int64_t)c.t.expert * p.m + c.t.c0;
+        const int col = kGated ? i % kUpScale : i;
+        const bool rows = wave < 4;
+        const char* base = rows ? reinterpret_cast<const char*>(p.x_scale + c.t.first + c.t.r0)
+                                : reinterpret_cast<const char*>(p.w_scale + at);
+        const int64_t bytes = rows ? c.rl * 4 : ((kGated ? p.n : 0) + c.cl) * 4;
+        uint32_t off = (uint32_t)i * 4;
+        if (!rows) off = col < c.cl ? (uint32_t)(col + (kGated && i >= kUpScale ? p.n : 0)) * 4 : kOutOfRange;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            __builtin_amdgcn_make_buffer_rsrc((void*)wave_uniform64((int64_t)base), 0,
+                                              __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000),
+            (__attribute__((address_space(3))) void*)(mem.scale[buf] + wave * 64), 4, (int)off, 0, 0, 0);
+        if (!kGated && p.bias != nullptr && (wave == 4 || wave == 5))
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                __builtin_amdgcn_make_buffer_rsrc((void*)wave_uniform64((int64_t)(p.bias + at)), 0,
+                                                  __builtin_amdgcn_readfirstlane(c.cl * 2), 0x00020000),
+                (__attribute__((address_space(3))) void*)(mem.bias[buf] + (wave - 4) * 64), 4, i * 4, 0, 0, 0);
+    };
+
+    const int lane = load.lane;
+    const int wm = wave / S::kWavesAcross, wn = wave % S::kWavesAcross;
+    const bool behind = wave >= 4;               // the second four waves run one interval behind
+    const uint32_t lds0 = lds_address(mem.tiles);
+    const uint32_t a_frag = lds0 + kPartA * kHalfBytes + frag_offset<true>(wm * 32 * S::kBlocks, lane);
+    const uint32_t b_frag = kSmall ? lds0 + kHalfBytes + frag_offset<true>(wn * 64, lane)
+                                   : lds0 + (kPartB + wn / 2) * kHalfBytes + frag_offset<true>(wn % 2 * 64, lane);
+    // More than loads run ahead, so that they reach a tile's end while it is
+    // multiplied and `next` is the one after it; past T's end they bring zeros.
+    int steps = (int)((p.k + kStepT - 1) / kStepT);
+    if (steps <= kAhead) steps = kAhead + 1;
+
+    Tile8 cur = tile_of(slot), next = tile_of(slot + grid);
+    Cursor8 at_b, at_a1;  // of small tiles' loads and of B and A's first half; of A's second half
+    at_b.aim(cur, row_bytes);
+    at_a1 = at_b;
+    // Loads of step `at` (of all tiles) into its stage.
+    auto load_small = [&](uint32_t at) __attribute__((always_inline)) {
+        load.small(at_b, at);
+        at_b.advance(steps, next, row_bytes);
+    };
+    auto load_b_a0 = [&](uint32_t at) __attribute__((always_inline)) {
+        load.b_a0(at_b, at);
+        at_b.advance(steps, next, row_bytes);
+    };
+    auto load_a1 = [&](uint32_t at) __attribute__((always_inline)) {
+        load.a1(at_a1, at);
+        at_a1.advance(steps, next, row_bytes);
+    };
+    if constexpr (kSmall) {
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) load_small(s);
+    } else {
+        load_b_a0(0);
+        load_a1(0);
+        load_b_a0(1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_loads<0>();
+    phase_barrier();
+    if (behind) phase_barrier();
+
+    // Vector-memory operations of a tile's end at least (the stores): younger than
+    // the next tile's first loads, they need not be waited for with these.
+    constexpr int kStores = S::kHalves * S::kBlocks * (kGated ? 2 : 4);
+    uint32_t at = 0;  // steps so far, of all tiles
+    int buf = 0;
+    for (int64_t id = slot; id < total; id += grid) {
+        load_scales(cur, buf);
+        TileSums8<kSmall, kCodes> sums;
+#pragma unroll
+        for (int h = 0; h < S::kHalves; ++h)
+#pragma unroll
+            for (int f = 0; f < S::kBlocks; ++f) sums.v[h][f][0] = sums.v[h][f][1] = typename Sum16<kCodes>::V{};
+
+        // The waits count operations younger than the loads that have to be there;
+        // where more are under way (scales, residual) they only wait for more.
+        auto run = [&](auto tag) __attribute__((always_inline)) {
+            constexpr bool kBoth = decltype(tag)::value != 0;  // the tile has rows in its second half
+            auto one_step = [&](auto extra) __attribute__((always_inline)) {
+                constexpr int kExtra = decltype(extra)::value;
+                Frags fb;
+                if constexpr (kSmall) {
+                    bf16x8 fa[1][4];
+                    const uint32_t stage = at % kSmallStages * kSmallStageBytes;
+                    load_small(at + kAhead);  // every wave has read that stage
+                    read_frags<true>(b_frag + stage, fb);
+                    read_block<true>(a_frag + stage, fa[0]);
+                    wait_loads<8 + kExtra>();  // step + 1; the two after (8) stay in flight
+                    phase_barrier();
+                    multiply8<kCodes>(fa, fb, sums.v[0]);
+                    phase_barrier();
+                } else {
+                    Frags fa;
+                    const uint32_t stage = at % 2 * kStageBytes;
+                    load_a1(at + 1);
+                    read_frags<true>(b_frag + stage, fb);
+                    read_frags<true>(a_frag + stage, fa);
+                    wait_loads<8 + kExtra>();  // A1 of this step; B, A0 (6) and A1 (2) of the next stay in flight
+                    phase_barrier();
+                    multiply8<kCodes>(fa.v, fb, sums.v[0]);
+                    phase_barrier();
+                    load_b_a0(at + 2);  // every wave has read this stage's B and A0
+                    if constexpr (kBoth) read_frags<true>(a_frag + stage + kHalfBytes, fa);
+                    wait_loads<8 + kExtra>();  // B, A0 of the next step; its A1 (2) and the B, A0 after (6) stay
+                    phase_barrier();
+                    if constexpr (kBoth) multiply8<kCodes>(fa.v, fb, sums.v[1]);
+                    phase_barrier();
+                }
+                ++at;
+            };
+            one_step(ActTag<kStores>{});
+            if constexpr (kSmall) one_step(ActTag<kStores>{});
+            for (int step = kSmall ? 2 : 1; step < steps; ++step) one_step(ActTag<0>{});
+        };
+        if (kSmall || cur.rl > 128) run(ActTag<1>{});
+        else run(ActTag<0>{});
+
+        // The tile's results, while the next one's loads are under way.
+        const int l = opaque_lane();
+        const int64_t row0 = cur.t.first + cur.t.r0;
+        const WaveBlock block(mem.blocks, wave, l);
+        const float* scale = mem.scale[buf];
+        auto row_scale = [&](int r) { return __int_as_float(lds_int(reinterpret_cast<const int*>(scale + r + l % 32))); };
+        const TileMatrix out(p.out + row0 * p.n + cur.t.c0, p.n, cur.t.c0, cur.rl, cur.cl);
+        if constexpr (kGated) {
+            const int col = wn * 32;
+            f32x4 gate[4], up[4];
+            lds_runs(scale + kColScale + col + l / 32 * 4, gate);
+            lds_runs(scale + kColScale + kUpScale + col + l / 32 * 4, up);
+            for_each_block<S>(wm, [&](int h, int f, int r) {
+                const float row = row_scale(r);
+                f32x16 v = scaled(sums.v[h][f][0], gate, row);
+                const f32x16 u = scaled(sums.v[h][f][1], up, row);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = act_value<kAct>(v[i]) * u[i];
+                store_block(block, out, r, col, l, v);
+            });
+        } else {
+            const TileMatrix res(p.residual + row0 * p.n + cur.t.c0, p.n, cur.t.c0, cur.rl, cur.cl);
+#pragma unroll
+            for (int cb = 0; cb < 2; ++cb) {
+                const int col = wn * 64 + cb * 32;
+                f32x4 cols[4];
+                u32x2 bias[4];
+                lds_runs(scale + kColScale + col + l / 32 * 4, cols);
+                if (p.bias != nullptr) lds_runs(mem.bias[buf] + (col + l / 32 * 4) / 2, bias);
+                for_each_block<S>(wm, [&](int h, int f, int r) {
+                    f32x16 v = scaled(sums.v[h][f][cb], cols, row_scale(r));
+                    if (p.bias != nullptr) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) add4(v, j, bias[j]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = act_value<kAct>(v[i]);
+                    if (p.residual != nullptr) {
+                        u32x4 rv[2];
+                        u32x2 runs[4];
+                        res.load(r, col, l, rv);
+                        block.to_runs(rv, runs);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) add4(v, j, runs[j]);
+                    }
+                    store_block(block, out, r, col, l, v);
+                });
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        cur = next;
+        next = tile_of(id + 2 * (int64_t)grid);
+        buf ^= 1;
+    }
+    if (!behind) phase_barrier();
+    wait_loads<0>();  // none into LDS that another workgroup may get
+}
+
+template <Codes8 kCodes, bool kGated, int kAct>
+hipError_t launch_product8(const Product8Params& p, bool small, bool once, int num_cus, hipStream_t stream) {
+    const unsigned blocks = workgroups(num_cus);
+    auto* kernel = !small ? expert_product8_kernel<kCodes, kGated, kAct, false, false>
+                   : once ? expert_product8_kernel<kCodes, kGated, kAct, true, true>
+                          : expert_product8_kernel<kCodes, kGated, kAct, true, false>;
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kTileThreads), 0, stream, p);
+    if (p.apart && hipPeekAtLastError() == hipSuccess)
+        hipLaunchKernelGGL((expert_product8_kernel<kCodes, kGated, kAct, true, false>), dim3(blocks),
+                           dim3(kTileThreads), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <Codes8 kCodes>
+hipError_t launch_tiles(const Product8Params& p, const Expert8BitArgs& a, bool small, bool once, int num_cus,
                         hipStream_t stream) {
     return with_activation(a.activation, [&](auto act) {
         constexpr int kAct = decltype(act)::value;
-        return a.gated ? launch_product<Product::kForward, true, kAct, kOp>(p, tiles.small, num_cus, stream)
-                       : launch_product<Product::kForward, false, kAct, kOp>(p, tiles.small, num_cus, stream);
+        return a.gated ? launch_product8<kCodes, true, kAct>(p, small, once, num_cus, stream)
+                       : launch_product8<kCodes, false, kAct>(p, small, once, num_cus, stream);
     });
 }
 
 }  // namespace
 
 hipError_t launch_expert_8bit(const Expert8BitArgs& a, int num_cus, hipStream_t stream) {
-    GemmParams p = params_of(a.rows, a.gated ? 2 * a.n : a.n, a.k / 2, a.x, a.w, a.y);
+    Product8Params p{};
+    p.off = a.rows.offsets;
+    p.num_experts = a.rows.num_experts;
+    p.max_rows = a.rows.max_rows;
+    p.m = a.gated ? 2 * a.n : a.n;
+    p.k = a.k / 2;
     p.n = a.n;
-    p.a_scale = a.x_scale;
-    p.b_scale = a.w_scale;
+    p.x = static_cast<const uint16_t*>(a.x);
+    p.w = static_cast<const uint16_t*>(a.w);
+    p.x_scale = a.x_scale;
+    p.w_scale = a.w_scale;
     p.bias = static_cast<const uint16_t*>(a.bias);
     p.residual = static_cast<const uint16_t*>(a.residual);
+    p.out = static_cast<uint16_t*>(a.y);
+    p.skip_rows = -1;
     const Stream8Plan plan = plan_stream8(a.rows.max_rows, a.rows.num_experts, p.m, a.k, num_cus);
     const bool streamed = plan.groups > 0;
     if (streamed) {
@@ -38,11 +538,13 @@ hipError_t launch_expert_8bit(const Expert8BitArgs& a, int num_cus, hipStream_t 
         const hipError_t err = launch_expert_stream8(a, plan, num_cus, stream);
         if (err != hipSuccess || a.rows.max_rows <= p.skip_rows) return err;  // no expert can have more
     }
-    TileChoice tiles = choose_tiles(a.rows.max_rows, most_groups(a.rows), a.n, a.gated ? 128 : 256, p.k, num_cus);
-    if (streamed) tiles = {true, false};
+    const int64_t groups = most_groups(a.rows);
+    TileChoice tiles = choose_tiles(a.rows.max_rows, groups, a.n, a.gated ? 128 : 256, p.k, num_cus);
+    const bool few = streamed || a.rows.max_rows <= 64 * groups;
+    if (few) tiles = {true, false};
     p.apart = tiles.apart;
-    return a.int8 ? launch_tiles<Operand::kInt8>(p, a, tiles, num_cus, stream)
-                  : launch_tiles<Operand::kFp8>(p, a, tiles, num_cus, stream);
+    return a.int8 ? launch_tiles<Codes8::kInt8>(p, a, tiles.small, few, num_cus, stream)
+                  : launch_tiles<Codes8::kFp8>(p, a, tiles.small, few, num_cus, stream);
 }
 
 }  // namespace moe

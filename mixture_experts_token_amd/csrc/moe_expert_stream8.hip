@@ -38,6 +38,7 @@ namespace moe {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;
 static_assert(kWaves == kStream8Waves, "the plan divides the waves");
@@ -84,19 +85,19 @@ __device__ __forceinline__ int expert_by_lanes(const int64_t* pre, int num_exper
     return first + __popcll(__ballot(lane < span && at < num_experts && pre[at < num_experts ? at : 0] <= id)) - 1;
 }
 
-template <Operand kOp>
+template <bool kInt8>
 struct Sum4 {
     typedef f32x4 V;
 };
 template <>
-struct Sum4<Operand::kInt8> {
+struct Sum4<true> {
     typedef i32x4 V;
 };
 
 // acc += the 16 x 16 products of 64 codes each.
-template <Operand kOp>
-__device__ __forceinline__ typename Sum4<kOp>::V multiply16(u32x4 w, u32x4 x, typename Sum4<kOp>::V acc) {
-    if constexpr (kOp == Operand::kInt8) {
+template <bool kInt8>
+__device__ __forceinline__ typename Sum4<kInt8>::V multiply16(u32x4 w, u32x4 x, typename Sum4<kInt8>::V acc) {
+    if constexpr (kInt8) {
         return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, x), acc,
                                                      0, 0, 0);
     } else {
@@ -126,9 +127,9 @@ __device__ __forceinline__ T own_of(T a, T b, T c, T d, int lane) {
     return lane & 2 ? hi : lo;
 }
 
-template <Operand kOp, bool kGated, int kAct, int kGroups>
+template <bool kInt8, bool kGated, int kAct, int kGroups>
 __global__ __launch_bounds__(kThreads, 2 * kPerCu<kGroups>) void expert_stream8_kernel(Stream8Params p) {
-    typedef typename Sum4<kOp>::V V;
+    typedef typename Sum4<kInt8>::V V;
     typedef decltype(V{}[0] + V{}[0]) T;             // float, or int for int8
     constexpr int kWaveCols = kGated ? kWaveRows / 2 : kWaveRows;   // output columns
     constexpr int kRows = 4 * kGroups;               // x rows of an item
@@ -232,7 +233,7 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<kGroups>) void expert_stream8_
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) acc[t][g] = multiply16<kOp>(wv[d][t], xv[d][g], acc[t][g]);
+                    for (int g = 0; g < kGroups; ++g) acc[t][g] = multiply16<kInt8>(wv[d][t], xv[d][g], acc[t][g]);
                 issue(d);
             }
         }
@@ -279,24 +280,24 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<kGroups>) void expert_stream8_
     }
 }
 
-template <Operand kOp, int kGroups>
+template <bool kInt8, int kGroups>
 hipError_t launch_rows(const Stream8Params& p, const Expert8BitArgs& a, int num_cus, hipStream_t stream) {
     return with_activation(a.activation, [&](auto act) {
         constexpr int kAct = decltype(act)::value;
-        auto* kernel = a.gated ? expert_stream8_kernel<kOp, true, kAct, kGroups>
-                               : expert_stream8_kernel<kOp, false, kAct, kGroups>;
+        auto* kernel = a.gated ? expert_stream8_kernel<kInt8, true, kAct, kGroups>
+                               : expert_stream8_kernel<kInt8, false, kAct, kGroups>;
         hipLaunchKernelGGL(kernel, dim3((unsigned)(num_cus * kPerCu<kGroups>)), dim3(kThreads), 0, stream, p);
         return hipGetLastError();
     });
 }
 
-template <Operand kOp>
+template <bool kInt8>
 hipError_t launch_kind(const Stream8Params& p, const Stream8Plan& plan, const Expert8BitArgs& a, int num_cus,
                        hipStream_t stream) {
     switch (plan.groups) {
-        case 1: return launch_rows<kOp, 1>(p, a, num_cus, stream);
-        case 2: return launch_rows<kOp, 2>(p, a, num_cus, stream);
-        default: return launch_rows<kOp, 4>(p, a, num_cus, stream);
+        case 1: return launch_rows<kInt8, 1>(p, a, num_cus, stream);
+        case 2: return launch_rows<kInt8, 2>(p, a, num_cus, stream);
+        default: return launch_rows<kInt8, 4>(p, a, num_cus, stream);
     }
 }
 
@@ -319,8 +320,8 @@ hipError_t launch_expert_stream8(const Expert8BitArgs& a, const Stream8Plan& pla
     p.bias = static_cast<const uint16_t*>(a.bias);
     p.residual = static_cast<const uint16_t*>(a.residual);
     p.out = static_cast<uint16_t*>(a.y);
-    return a.int8 ? launch_kind<Operand::kInt8>(p, plan, a, num_cus, stream)
-                  : launch_kind<Operand::kFp8>(p, plan, a, num_cus, stream);
+    return a.int8 ? launch_kind<true>(p, plan, a, num_cus, stream)
+                  : launch_kind<false>(p, plan, a, num_cus, stream);
 }
 
 }  // namespace moe

@@ -34,14 +34,6 @@ namespace moe {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
-typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-
-// What the operands are.  8-bit ones are loaded and read as half as many bf16 (T
-// counts pairs of codes, 16-byte vectors hold 16): every T-contiguous step of 128
-// bytes a row is then a step of 128 codes at the same number of MFMA cycles.
-enum class Operand { kBf16, kInt8, kFp8 };
 
 constexpr int kStepT = 64;
 constexpr int kTileThreads = 512;
@@ -145,8 +137,9 @@ __device__ __forceinline__ uint32_t load_offset(int64_t rows_bytes, int wave_row
     }
 }
 
-// This wave's two loads of a half tile into `dst` (the half tile's LDS).
-template <bool kTContig>
+// This wave's two loads of a half tile into `dst` (the half tile's LDS).  kOnce:
+// non-temporal.
+template <bool kTContig, bool kOnce = false>
 __device__ __forceinline__ void load_half(char* dst, __amdgpu_buffer_rsrc_t rsrc, const uint32_t (&voff)[2],
                                           uint32_t half_offset, int rem, int wave, int lane) {
 #pragma unroll
@@ -154,7 +147,8 @@ __device__ __forceinline__ void load_half(char* dst, __amdgpu_buffer_rsrc_t rsrc
         uint32_t off = voff[i] + half_offset;
         if constexpr (kTContig) off = t_slot(i * 8 + lane / 8, lane % 8) < rem ? off : kOutOfRange;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rsrc, (__attribute__((address_space(3))) void*)(dst + (wave * 2 + i) * 1024), 16, (int)off, 0, 0, 0);
+            rsrc, (__attribute__((address_space(3))) void*)(dst + (wave * 2 + i) * 1024), 16, (int)off, 0, 0,
+            kOnce ? 2 : 0);
     }
 }
 
@@ -283,18 +277,10 @@ __device__ __forceinline__ void read_block(uint32_t a, bf16x8 (&fr)[4]) {
 // a small tile has h = f = 0, row 32 wm + l % 32.
 // a_sum: with kSumA, row 128 h + 64 wm + 32 f + l % 32 of operand a summed over
 // the T that lane l's fragments hold (the other half of them is in lane l ^ 32).
-template <Operand kOp>
-struct SumType {
-    typedef f32x16 V;
-};
-template <>
-struct SumType<Operand::kInt8> {
-    typedef i32x16 V;
-};
-template <bool kSmall, Operand kOp = Operand::kBf16>
+template <bool kSmall>
 struct TileSums {
     typedef TileShape<kSmall> S;
-    typename SumType<kOp>::V v[S::kHalves][S::kBlocks][2];
+    f32x16 v[S::kHalves][S::kBlocks][2];
     float a_sum[S::kHalves][S::kBlocks];
 };
 
@@ -312,37 +298,18 @@ __device__ __forceinline__ float sum8(bf16x8 frag, float v) {
     return v;
 }
 
-// Two fragments of 16 codes as one of 32 (which of T a lane holds does not
-// matter, as long as both operands hold the same).
-__device__ __forceinline__ i32x8 join(bf16x8 lo, bf16x8 hi) {
-    return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
 // acc += a b over a step.
-template <bool kSumA, Operand kOp, int kBlocks>
-__device__ __forceinline__ void multiply(const bf16x8 (&a)[kBlocks][4], const Frags& b,
-                                         typename SumType<kOp>::V (&acc)[kBlocks][2], float (&a_sum)[kBlocks]) {
-    static_assert(!kSumA || kOp == Operand::kBf16, "sums of operand a are the bias gradient's");
+template <bool kSumA, int kBlocks>
+__device__ __forceinline__ void multiply(const bf16x8 (&a)[kBlocks][4], const Frags& b, f32x16 (&acc)[kBlocks][2],
+                                         float (&a_sum)[kBlocks]) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-        if constexpr (kOp == Operand::kFp8) {
-            if (s % 2) continue;
-        }
 #pragma unroll
         for (int f = 0; f < kBlocks; ++f)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if constexpr (kOp == Operand::kBf16)
-                    acc[f][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[c][s], a[f][s], acc[f][c], 0, 0, 0);
-                else if constexpr (kOp == Operand::kInt8)
-                    acc[f][c] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, b.v[c][s]),
-                                                                      __builtin_bit_cast(i32x4, a[f][s]), acc[f][c], 0,
-                                                                      0, 0);
-                else  // format 0 of both is E4M3; scales of 0 select the form without scales
-                    acc[f][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                        join(b.v[c][s], b.v[c][s + 1]), join(a[f][s], a[f][s + 1]), acc[f][c], 0, 0, 0, 0, 0, 0);
-            }
+            for (int c = 0; c < 2; ++c)
+                acc[f][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[c][s], a[f][s], acc[f][c], 0, 0, 0);
         if constexpr (kSumA) {
 #pragma unroll
             for (int f = 0; f < kBlocks; ++f) a_sum[f] = sum8(a[f][s], a_sum[f]);
@@ -418,14 +385,14 @@ __device__ __forceinline__ void begin_tile(char* lds, const TileOperands& o) {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <bool kSmall, Operand kOp>
-__device__ __forceinline__ void clear_sums(TileSums<kSmall, kOp>& sums) {
+template <bool kSmall>
+__device__ __forceinline__ void clear_sums(TileSums<kSmall>& sums) {
     typedef TileShape<kSmall> S;
 #pragma unroll
     for (int h = 0; h < S::kHalves; ++h)
 #pragma unroll
         for (int f = 0; f < S::kBlocks; ++f) {
-            sums.v[h][f][0] = sums.v[h][f][1] = typename SumType<kOp>::V{};
+            sums.v[h][f][0] = sums.v[h][f][1] = f32x16{};
             sums.a_sum[h][f] = 0.0f;
         }
 }
@@ -436,9 +403,9 @@ __device__ __forceinline__ void clear_sums(TileSums<kSmall, kOp>& sums) {
 // `fresh`: none were.  second_half: the tile has rows in its second half (the
 // barriers are the same without; its reads and MFMAs are left out).  On return
 // no load is in flight and every wave is done with LDS.
-template <bool kATc, bool kBTc, int kStores, bool kSumA, Operand kOp>
+template <bool kATc, bool kBTc, int kStores, bool kSumA>
 __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool fresh, bool second_half,
-                                          TileSums<false, kOp>& sums) {
+                                          TileSums<false>& sums) {
     static_assert(8 + kStores < 64, "vector-memory counter range");
     const TileLoader<kATc, kBTc> load(lds, o);
     const int lane = load.lane, wm = load.wave / 4, wn = load.wave % 4;
@@ -464,13 +431,13 @@ __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool
             read_frags<kATc>(a_frag + stage, fa);
             wait_loads<8 + kExtra>();  // A1 of this step; B, A0 (6) and A1 (2) of the next stay in flight
             phase_barrier();
-            multiply<kSumA, kOp>(fa.v, fb, sums.v[0], sums.a_sum[0]);
+            multiply<kSumA>(fa.v, fb, sums.v[0], sums.a_sum[0]);
             phase_barrier();
             load.b_a0(step + 2);       // into this stage: every wave has read its B and A0
             if constexpr (kBoth) read_frags<kATc>(a_frag + stage + kHalfBytes, fa);
             wait_loads<8 + kExtra>();  // B, A0 of the next step; its A1 (2) and the B, A0 after (6) stay in flight
             phase_barrier();
-            if constexpr (kBoth) multiply<kSumA, kOp>(fa.v, fb, sums.v[1], sums.a_sum[1]);
+            if constexpr (kBoth) multiply<kSumA>(fa.v, fb, sums.v[1], sums.a_sum[1]);
             phase_barrier();
         };
         if (steps > 0) one_step(0, ActTag<kStores>{});
@@ -485,9 +452,8 @@ __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool
 
 // The same for a small tile: one phase a step (8 MFMAs a wave on 12 KiB of
 // fragments), three steps of loads ahead.
-template <bool kATc, bool kBTc, int kStores, bool kSumA, Operand kOp>
-__device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool fresh, bool,
-                                          TileSums<true, kOp>& sums) {
+template <bool kATc, bool kBTc, int kStores, bool kSumA>
+__device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool fresh, bool, TileSums<true>& sums) {
     static_assert(8 + kStores < 64, "vector-memory counter range");
     const TileLoader<kATc, kBTc> load(lds, o);
     const int lane = load.lane, wm = load.wave / 2, wn = load.wave % 2;
@@ -511,7 +477,7 @@ __device__ __forceinline__ void tile_sums(char* lds, const TileOperands& o, bool
         read_block<kATc>(a_frag + stage, fa[0]);
         wait_loads<8 + decltype(extra)::value>();     // step + 1; the two after (8) stay in flight
         phase_barrier();
-        multiply<kSumA, kOp>(fa, fb, sums.v[0], sums.a_sum[0]);
+        multiply<kSumA>(fa, fb, sums.v[0], sums.a_sum[0]);
         phase_barrier();
     };
     if (steps > 0) one_step(0, ActTag<kStores>{});

@@ -17,6 +17,7 @@ using namespace moe::api;
 
 namespace {
 
+constexpr int64_t kMaxOutputs = int64_t(1) << 42;  // tiles of them are counted in 32 bits
 // k codes of magnitude 128 each way sum to at most k 2^14, which 32 bits hold.
 constexpr int64_t kMaxInt8Depth = (int64_t(1) << 17) - 16;
 
@@ -68,6 +69,7 @@ moe_status_t layer_impl(bool gated, bool int8, const void* x, const float* x_sca
     if (activation < MOE_ACT_NONE || activation > MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
     const moe_status_t st = check_rows(off, num_experts, max_rows);
     if (st != MOE_OK) return st;
+    if (max_rows > kMaxOutputs / n) return MOE_ERR_INVALID_ARG;
     if (n % 8 != 0 || k % 16 != 0) return MOE_ERR_MISALIGNED;
     if (w == nullptr || w_scale == nullptr) return MOE_ERR_INVALID_ARG;
     if (max_rows > 0 && (x == nullptr || x_scale == nullptr || y == nullptr)) return MOE_ERR_INVALID_ARG;
