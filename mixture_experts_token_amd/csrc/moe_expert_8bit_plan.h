@@ -25,16 +25,31 @@ inline int stream8_steps(int64_t k, int kw) {
     return (int)((mine + kStream8InFlight - 1) / kStream8InFlight * kStream8InFlight);
 }
 
+// Streamed / in tiles, us, at r rows per expert (n x k, evenly spread):
+//                                    r 1        4          8          12         16
+//   14336 x 4096 gated, 8 experts     107 / 154  146 / 196  149 / 196  167 / 198  220 / 198
+//   768 x 2048 gated, 128              46 / 59    67 / 85    73 / 86    80 / 87   103 / 87
+//   7168 x 2048 gated, 64             181 / 237  275 / 356  295 / 369  324 / 374  430 / 378
+//   2048 x 768 linear fp8, 128         31 / 45    41 / 61    48 / 62    53 / 62    66 / 62
+// Rows per pass: 4 to one row per expert (8 or 16 are up to 10 % slower there), 8 to
+// two (16: 5 - 10 % slower linear, equal gated), 16 beyond.  An expert of many rows
+// would have its weights read once for each 4, 8 or 16 of them: past four passes the
+// tiles take it, in a second launch (128 experts, 768 x 2048 gated, popularity rank
+// ^ -1.2, 6 rows on average: one pass 67, four 75, eight 65; 12 rows 71, 81, 89; 64
+// experts of 7168 x 2048, 12 rows 270, 301, 336: past 6 rows, two passes).
+// Waves per weight row: as many as leave 8 steps each, or 4 where the items would
+// not fill the GPU (one expert, one row, 4096 x 4096: 10.8 us with 8, 9.1 with 4;
+// 8 experts, 2 rows, 14336 x 4096 gated 150 / 160).
 // cols: weight rows of an expert (n, or 2 n gated).
 inline Stream8Plan plan_stream8(int64_t max_rows, int64_t num_experts, int64_t cols, int64_t k, int num_cus) {
     Stream8Plan p = {0, 0, 0, 0};
-    if (max_rows > 16 * num_experts) return p;
-    p.groups = max_rows > 4 * num_experts ? 4 : max_rows > 2 * num_experts ? 2 : 1;
-    p.most_rows = 4 * 4 * p.groups;
+    if (max_rows > 12 * num_experts) return p;
+    p.groups = max_rows > 2 * num_experts ? 4 : max_rows > num_experts ? 2 : 1;
+    p.most_rows = (max_rows > 6 * num_experts ? 2 : 4) * 4 * p.groups;
     const int64_t used = max_rows < num_experts ? max_rows : num_experts;
     for (p.kw = kStream8Waves; p.kw > 1; p.kw /= 2) {
         const int steps = stream8_steps(k, p.kw);
-        const int64_t rows = kStream8Waves / (p.kw / 2) * kStream8WaveRows;  // of an item with half as many
+        const int64_t rows = kStream8Waves / (p.kw / 2) * kStream8WaveRows;  // of an item with half as many waves
         if (steps >= 8 || (steps >= 4 && used * ((cols + rows - 1) / rows) < 2 * num_cus)) break;
     }
     p.steps = stream8_steps(k, p.kw);

@@ -137,9 +137,8 @@ __device__ __forceinline__ uint32_t load_offset(int64_t rows_bytes, int wave_row
     }
 }
 
-// This wave's two loads of a half tile into `dst` (the half tile's LDS).  kOnce:
-// non-temporal.
-template <bool kTContig, bool kOnce = false>
+// This wave's two loads of a half tile into `dst` (the half tile's LDS).
+template <bool kTContig>
 __device__ __forceinline__ void load_half(char* dst, __amdgpu_buffer_rsrc_t rsrc, const uint32_t (&voff)[2],
                                           uint32_t half_offset, int rem, int wave, int lane) {
 #pragma unroll
@@ -147,8 +146,7 @@ __device__ __forceinline__ void load_half(char* dst, __amdgpu_buffer_rsrc_t rsrc
         uint32_t off = voff[i] + half_offset;
         if constexpr (kTContig) off = t_slot(i * 8 + lane / 8, lane % 8) < rem ? off : kOutOfRange;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rsrc, (__attribute__((address_space(3))) void*)(dst + (wave * 2 + i) * 1024), 16, (int)off, 0, 0,
-            kOnce ? 2 : 0);
+            rsrc, (__attribute__((address_space(3))) void*)(dst + (wave * 2 + i) * 1024), 16, (int)off, 0, 0, 0);
     }
 }
 
