@@ -114,17 +114,19 @@ struct Int8Codes {
 
     template <bool kBF16>
     __device__ static __forceinline__ uint32_t vec_amax(const u32x4& v) {
-        uint32_t m = 0;
+        if constexpr (kBF16) {
+            typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+            u16x2 m = {0, 0};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if constexpr (kBF16) {
-                m = larger(m, (v[q] << 16) & 0x7FFFFFFFu);
-                m = larger(m, v[q] & 0x7FFF0000u);
-            } else {
-                m = larger(m, v[q] & 0x7FFFFFFFu);
-            }
+            for (int q = 0; q < 4; ++q)
+                m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, (uint32_t)(v[q] & 0x7FFF7FFFu)));
+            return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+        } else {
+            uint32_t m = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = larger(m, v[q] & 0x7FFFFFFFu);
+            return m;
         }
-        return m;
     }
     __device__ static __forceinline__ uint32_t larger(uint32_t m, uint32_t o) { return o > m ? o : m; }
     __device__ static __forceinline__ float scale(uint32_t m) {
@@ -160,16 +162,50 @@ struct Int8Codes {
     __device__ static __forceinline__ uint32_t pack(int a, int b, int c, int d) {
         return (a & 0xFF) | (b & 0xFF) << 8 | (c & 0xFF) << 16 | (uint32_t)d << 24;
     }
-    template <bool kBF16>
-    __device__ static __forceinline__ u32x2 vec_codes(const u32x4& v, float scale) {
+    // Codes of 4 kWords elements.  x (1 / s) plus 1.5 2^23, rounded once, has the
+    // nearest integer in its low bits.  1 / s is within 2^-24 of it, so the integer is
+    // the one nearest to x / s unless x / s lies within 127 2^-24 of a tie; the
+    // remainder tells, and Nearest does those vectors (one in a thousand of random
+    // ones).  Nearest for all took three times the operations: 8192 rows of
+    // 14336 bf16 89 us, 71 with this (moe_quantize_rows as it then was).
+    template <int kWords>
+    __device__ static __forceinline__ u32x2 codes(const float (&x)[4 * kWords], float scale) {
+        constexpr float kMagic = 12582912.0f;
         const Nearest n(scale);
         if (!n.finite) return u32x2{0u, 0u};
-        if constexpr (kBF16)
-            return u32x2{pack(n(bf16_lo(v[0])), n(bf16_hi(v[0])), n(bf16_lo(v[1])), n(bf16_hi(v[1]))),
-                         pack(n(bf16_lo(v[2])), n(bf16_hi(v[2])), n(bf16_lo(v[3])), n(bf16_hi(v[3])))};
-        else
-            return u32x2{pack(n(__uint_as_float(v[0])), n(__uint_as_float(v[1])), n(__uint_as_float(v[2])),
-                              n(__uint_as_float(v[3]))), 0u};
+        uint32_t u[4 * kWords];
+        float off = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4 * kWords; ++i) {
+            const float m = __builtin_fmaf(x[i], n.r, kMagic);
+            u[i] = __float_as_uint(m);
+            off = __builtin_fmaxf(off, __builtin_fabsf(__builtin_fmaf(kMagic - m, scale, x[i])));
+        }
+        u32x2 out = {0u, 0u};
+        if (n.up != 1.0f || off >= scale * (0.5f - 0x1p-16f)) {
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) out[w] = pack(n(x[4 * w]), n(x[4 * w + 1]), n(x[4 * w + 2]), n(x[4 * w + 3]));
+        } else {
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                const uint32_t lo = __builtin_amdgcn_perm(u[4 * w + 1], u[4 * w], 0x0c0c0400u);
+                const uint32_t hi = __builtin_amdgcn_perm(u[4 * w + 3], u[4 * w + 2], 0x04000c0cu);
+                out[w] = lo | hi;
+            }
+        }
+        return out;
+    }
+    template <bool kBF16>
+    __device__ static __forceinline__ u32x2 vec_codes(const u32x4& v, float scale) {
+        if constexpr (kBF16) {
+            const float x[8] = {bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1]),
+                                bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3])};
+            return codes<2>(x, scale);
+        } else {
+            const float x[4] = {__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]),
+                                __uint_as_float(v[3])};
+            return codes<1>(x, scale);
+        }
     }
 };
 
