@@ -63,7 +63,8 @@ struct Bf16Quotient {
 // the float quotient.
 struct E4M3Codes {
     typedef float Amax;
-    static constexpr bool kGroups = true;  // scales of groups within a row too
+    static constexpr bool kGroups = true;       // scales of groups within a row too
+    static constexpr bool kPlainStores = true;  // of large permuted outputs
 
     // Largest |x| of one 16-byte vector (NaN never wins a comparison, as in the
     // reading of amax: the largest of the comparable magnitudes).
@@ -110,7 +111,7 @@ struct E4M3Codes {
 // is NaN and the element does not pass unnoticed.
 struct Int8Codes {
     typedef uint32_t Amax;
-    static constexpr bool kGroups = false;
+    static constexpr bool kGroups = false, kPlainStores = false;
 
     template <bool kBF16>
     __device__ static __forceinline__ uint32_t vec_amax(const u32x4& v) {
