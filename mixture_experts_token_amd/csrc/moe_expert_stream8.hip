@@ -92,7 +92,8 @@ struct Sum4<true> {
     typedef i32x4 V;
 };
 
-// acc += the 16 x 16 products of 64 codes each.
+// acc += the 16 x 16 products of 64 codes each (fp8: see Codes8 in
+// moe_expert_8bit.hip for what the instruction adds with fewer bits).
 template <bool kInt8>
 __device__ __forceinline__ typename Sum4<kInt8>::V multiply16(u32x4 w, u32x4 x, typename Sum4<kInt8>::V acc) {
     if constexpr (kInt8) {

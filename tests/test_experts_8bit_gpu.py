@@ -96,6 +96,12 @@ SHAPES = [
     ([1500, 0, 700, 257, 1000, 3], 3864, 528),
     ([700, 0, 1, 410], 1800, 2000),
     ([1024, 1025, 1134, 1023], 3960, 1040),
+    # more experts than lanes look at once, in tiles; rows per expert at which the
+    # streamed rows per pass change, with experts of more passes than are streamed
+    ([13 + e % 3 for e in range(1024)], 24, 48),
+    ([2, 1, 2, 30, 0, 2, 3, 1, 0, 1], 72, 784),
+    ([3, 9, 16, 17, 0, 1, 70, 4], 264, 2064),
+    ([1, 2, 0, 1, 0, 0, 17, 0, 1, 0, 1, 0] * 2, 40, 1296),
 ]
 ACTS = ["silu", "gelu_tanh", "relu", "none"]
 
@@ -138,6 +144,32 @@ def test_linear(hip_device, shape, kind, act, bias, residual):
     LAYER["linear", kind](x, xs, w, ws, off, y, bias=b, residual=r, activation=act)
     torch.cuda.synchronize()
     E8.check_linear(x, xs, w, ws, b, r, off, kind, act, y)
+    assert_untouched(y[m:], "y behind the last expert")
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=_id)
+def test_fp8_sums_of_small_whole_numbers_are_exact(hip_device, shape):
+    """Codes of whole numbers up to 8: products of at most 64, of which nothing is cut
+    (2^(6 - 13) is below one), and sums below 2^24."""
+    counts, n, k = shape
+    dev, m, e = hip_device, sum(shape[0]), len(shape[0])
+    _say("fp8 exact %s" % _id(shape))
+    g = torch.Generator(device="cpu").manual_seed(11)
+    off = offsets(counts, dev)
+
+    def whole(*size):
+        return torch.randint(-8, 9, size, generator=g).float().to(torch.float8_e4m3fn)
+
+    x, w = whole(m + TAIL, k), whole(e, n, k)
+    xs = 2.0 ** torch.randint(-3, 3, (m + TAIL,), generator=g)
+    ws = 2.0 ** torch.randint(-3, 3, (e, n), generator=g)
+    y = poisoned((m + TAIL, n), BF16, dev)
+    moe.moe_grouped_linear_fp8(x.to(dev), xs.to(dev), w.to(dev), ws.to(dev), off, y)
+    torch.cuda.synchronize()
+    want = torch.zeros(m, n, dtype=torch.float64)
+    for i, lo, hi in X.segments(off):
+        want[lo:hi] = (x[lo:hi].double() @ w[i].double().t()) * xs[lo:hi, None] * ws[i]
+    assert torch.equal(y[:m].cpu(), want.float().to(BF16))
     assert_untouched(y[m:], "y behind the last expert")
 
 
@@ -438,6 +470,67 @@ def test_row_offsets_past_32_bits(hip_device, kind):
         want, want_scale = E8.codes_of(v[lo:hi].cpu(), kind)
         assert torch.equal(codes[lo:hi].cpu(), want.view(torch.uint8)) and torch.equal(scale[lo:hi].cpu(), want_scale)
     assert_untouched(codes[last:], "codes behind the last expert")
+
+
+@pytest.mark.parametrize("counts", [[1], [10, 0, 3], [40, 60], [300]], ids=str)
+@pytest.mark.parametrize("kind", KINDS)
+def test_longest_rows(hip_device, kind, counts):
+    """Codes of one against codes of one and of nought: the sum is the number of ones, which fp32 holds."""
+    dev, n, k = hip_device, 40, 2**20 if kind == "fp8" else 131056
+    m, e = sum(counts), len(counts)
+    off = offsets(counts, dev)
+    one = torch.ones(1).to(CODE[kind]).view(torch.uint8).item()
+    x = torch.full((m, k), one, dtype=torch.uint8, device=dev).view(CODE[kind])
+    w = torch.zeros((e, n, k), dtype=torch.uint8, device=dev)
+    for c in range(n):
+        w[:, c, : k - 16 * c].fill_(one)
+        w[:, c, k - 1].fill_(one)
+    y = poisoned((m, n), BF16, dev)
+    LAYER["linear", kind](x, torch.full((m,), 0.5, device=dev), w.view(CODE[kind]), torch.ones(e, n, device=dev), off, y)
+    torch.cuda.synchronize()
+    want = torch.tensor([k if c == 0 else k - 16 * c + 1 for c in range(n)], dtype=torch.float64) * 0.5
+    assert torch.equal(y.cpu(), want.float().to(BF16).expand(m, n))
+
+
+@pytest.mark.parametrize("counts", [[1, 0], [9, 2], [50, 90]], ids=str)
+@pytest.mark.parametrize("kind", KINDS)
+def test_most_columns(hip_device, kind, counts):
+    dev, n, k = hip_device, 2**20, 16
+    m, e = sum(counts), len(counts)
+    off = offsets(counts, dev)
+    x, xs = row_codes(counts, k, kind, 1, dev)
+    w, ws = rand_codes((e, 2 * n, k), kind, 3, dev), rand_scale((e, 2 * n), 4, dev, 1e-3)
+    h = poisoned((m + TAIL, n), BF16, dev)
+    LAYER["gated", kind](x, xs, w, ws, off, h)
+    torch.cuda.synchronize()
+    cols = torch.cat([torch.arange(0, 300), torch.arange(n // 2 - 150, n // 2 + 150), torch.arange(n - 300, n)]).to(dev)
+    both = torch.cat([cols, cols + n])
+    E8.check_gated(x, xs, w.view(torch.uint8)[:, both].view(CODE[kind]), ws[:, both], off, kind, "silu", h[:, cols])
+    assert_untouched(h[m:], "h behind the last expert")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("counts,max_rows", [([1, 0, 2], 4000), ([1, 0, 2], 30), ([40, 0, 3], 900), ([300, 5, 0], 5000),
+                                             ([130, 0, 257], 387)], ids=str)
+def test_buffers_larger_than_the_rows(hip_device, kind, counts, max_rows):
+    """The choice of kernels goes by the buffers' rows, the work by the offsets."""
+    dev, n, k = hip_device, 200, 528
+    m, e = sum(counts), len(counts)
+    off = offsets(counts, dev)
+    x, xs = row_codes(counts + [max_rows - m], k, kind, 1, dev)
+    xs[m:] = float("nan")
+    w, ws = rand_codes((e, n, k), kind, 3, dev), rand_scale((e, n), 4, dev, 1e-3)
+    b, r = randn((e, n), 5, dev), randn((max_rows + TAIL, n), 6, dev)
+    y = poisoned((max_rows + TAIL, n), BF16, dev)
+    LAYER["linear", kind](x, xs, w, ws, off, y, bias=b, residual=r, activation="silu")
+    h = poisoned((max_rows + TAIL, n // 2 // 8 * 8), BF16, dev)
+    wg, wgs = w[:, :2 * h.shape[1]].contiguous(), ws[:, :2 * h.shape[1]].contiguous()
+    LAYER["gated", kind](x, xs, wg, wgs, off, h, activation="relu")
+    torch.cuda.synchronize()
+    E8.check_linear(x, xs, w, ws, b, r, off, kind, "silu", y)
+    E8.check_gated(x, xs, wg, wgs, off, kind, "relu", h)
+    assert_untouched(y[m:], "y behind the last expert")
+    assert_untouched(h[m:], "h behind the last expert")
 
 
 @pytest.mark.parametrize("counts", [[0, 1, 1], [0, 90, 200]], ids=str)
