@@ -1,7 +1,7 @@
 // moe_expert_stream8.hip -- the experts' layers on int8 and fp8 codes for experts
 // with few rows each (single tokens and small batches).
 //
-// The same results as the tiles of moe_expert_8bit.hip; the work is reading the
+// The same products as the tiles of moe_expert_8bit.hip; the work is reading the
 // experts' weights once, the bound is HBM.  fp8 has no dot product on the vector
 // units, and int8's take an instruction per four weights and x row, so the
 // products run on the matrix cores here too, though few of their outputs are
@@ -15,14 +15,18 @@
 //     / 4, its quarter r % 4" of every 64 bytes; x is loaded the same way, 4 rows
 //     at a time.  Of the 16 x 16 outputs those whose two quarters agree are wanted:
 //     one of the four that a lane gets, and four neighbouring lanes' add up to a
-//     dot product.  A quarter of the matrix work is used; it is a fifth of the time
-//     at 4 x rows.
+//     dot product.  A quarter of the matrix work is used.
 //   * A wave takes 16 weight rows (gated: 8 gate rows and their 8 up rows), a
 //     step is 256 bytes of each, and the kw waves of a group take the steps of the
 //     same rows in turn.  Loads run kInFlight steps ahead, past the end of an item
 //     into the next one, so reading does not stop for the sums.
 //   * The kw waves' sums meet in LDS in a fixed order; there activation and
 //     product, or the linear layer's epilogue, follow.
+//   * With 16 x rows (expert_stream8_whole_kernel) four loads are exchanged between
+//     neighbouring lanes instead, and all outputs are wanted.
+//
+// 256 experts, 2048 x 7168 gated, a row each on average: 687 us, 7.0 TB/s; eight of
+// them with a row: 37.6 us, 6.3 TB/s.
 
 #include <hip/hip_runtime.h>
 
