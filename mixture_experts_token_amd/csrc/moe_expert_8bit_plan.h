@@ -38,8 +38,10 @@ inline int stream8_steps(int64_t k, int kw) {
 // ^ -1.2, 6 rows on average: one pass 67, four 75, eight 65; 12 rows 71, 81, 89; 64
 // experts of 7168 x 2048, 12 rows 270, 301, 336: past 6 rows, two passes).
 // Waves per weight row: as many as leave 8 steps each, or 4 where the items would
-// not fill the GPU (one expert, one row, 4096 x 4096: 10.8 us with 8, 9.1 with 4;
-// 8 experts, 2 rows, 14336 x 4096 gated 150 / 160).
+// not be one per CU (one expert, one row, 4096 x 4096: 10.8 us with 8, 9.1 with 4;
+// 8 experts, 2 rows, 14336 x 4096 gated 150 / 160; up to two items per CU 4 instead
+// of 8 mostly cost 3 - 7 %: 8 of 256 experts, 7168 x 2048 23.4 / 24.5, 4 of 4096 x
+// 4096 13.9 / 14.9, but 6 of 3000 x 2000 gated 22.5 / 20.0).
 // cols: weight rows of an expert (n, or 2 n gated).
 inline Stream8Plan plan_stream8(int64_t max_rows, int64_t num_experts, int64_t cols, int64_t k, int num_cus) {
     Stream8Plan p = {0, 0, 0, 0};
@@ -50,7 +52,7 @@ inline Stream8Plan plan_stream8(int64_t max_rows, int64_t num_experts, int64_t c
     for (p.kw = kStream8Waves; p.kw > 1; p.kw /= 2) {
         const int steps = stream8_steps(k, p.kw);
         const int64_t rows = kStream8Waves / (p.kw / 2) * kStream8WaveRows;  // of an item with half as many waves
-        if (steps >= 8 || (steps >= 4 && used * ((cols + rows - 1) / rows) < 2 * num_cus)) break;
+        if (steps >= 8 || (steps >= 4 && used * ((cols + rows - 1) / rows) < num_cus)) break;
     }
     p.steps = stream8_steps(k, p.kw);
     return p;
