@@ -34,7 +34,7 @@
  *          even, within +-127.  A row with a NaN has the scale NaN, one with an
  *          infinity the scale infinity, and both codes of 0: what is computed
  *          from such a row is NaN.
- *   fp8    scale = amax / 448, one float division (1 where amax is 0; a NaN does
+ *   fp8    scale = amax / 448, one float division (1 where that is 0; a NaN does
  *          not count); code = E4M3FN of the float quotient x / scale, nearest,
  *          ties to even, saturated at +-448; a NaN quotient gives 0x7F.
  */

@@ -222,7 +222,7 @@ moe_status_t moe_permute_local(const void *hidden_states, int32_t dtype, const f
  *
  * Per group of group_size consecutive elements of a token row (group_size 0:
  * the whole row, one scale per token):
- *     scale = amax / 448 as one float division (1 when amax is 0; NaN
+ *     scale = amax / 448 as one float division (1 when that is 0; NaN
  *             elements do not count towards amax)
  *     code  = E4M3FN(x / scale): the float quotient rounded to the nearest
  *             code, ties to even, saturated at +-448; a NaN quotient -> 0x7F

@@ -59,8 +59,8 @@ struct Bf16Quotient {
     }
 };
 
-// fp8 E4M3FN: scale = amax / 448 (1 when amax is 0, NaN does not count), code of
-// the float quotient.
+// fp8 E4M3FN: scale = amax / 448 (1 when that is 0: also for an f32 amax below 448
+// 2^-150; NaN does not count), code of the float quotient.
 struct E4M3Codes {
     typedef float Amax;
     static constexpr bool kGroups = true;       // scales of groups within a row too
@@ -85,7 +85,10 @@ struct E4M3Codes {
         return m;
     }
     __device__ static __forceinline__ float larger(float m, float o) { return o > m ? o : m; }
-    __device__ static __forceinline__ float scale(float m) { return m > 0.0f ? __fdiv_rn(m, kE4M3Max) : 1.0f; }
+    __device__ static __forceinline__ float scale(float m) {
+        const float s = __fdiv_rn(m, kE4M3Max);
+        return s == 0.0f ? 1.0f : s;
+    }
 
     // Codes of one 16-byte vector: 8 bf16 -> 8 bytes, or 4 f32 -> 4 bytes (in .x).
     template <bool kBF16>

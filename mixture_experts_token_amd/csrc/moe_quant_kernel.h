@@ -8,7 +8,7 @@
 // permute of vLLM PR #14568 ("permute/unpermute kernel for moe optimization",
 // PR description) moves.  fp8, per group of consecutive elements (the whole row
 // when there is one scale per token): scale = amax / 448 as one float
-// division (1 when amax is 0); code = E4M3FN of the float quotient x / scale,
+// division (1 when that is 0); code = E4M3FN of the float quotient x / scale,
 // rounded to nearest with ties to even and saturated at 448; a NaN quotient
 // gets the code 0x7F.  int8, per row: Int8Codes (moe_quant_device.h).
 //

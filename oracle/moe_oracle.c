@@ -376,7 +376,7 @@ uint8_t oracle_double_to_e4m3(double x)
 /* row is cut into groups of `group` consecutive elements (group = h: one     */
 /* scale per token); per group                                                */
 /*   amax  = the largest |x| (exact),                                         */
-/*   scale = amax / 448 as one float division (1 when amax is 0),             */
+/*   scale = amax / 448 as one float division (1 when that is 0),             */
 /*   code  = E4M3FN of the float quotient x / scale (one float division,      */
 /*           then the rounding above); a NaN quotient (a NaN input, or inf /  */
 /*           inf) gets the positive NaN code 0x7F, whatever its sign bit.     */
@@ -400,6 +400,8 @@ int oracle_quantize_fp8_rows(const void *x, int x_is_bf16, int64_t rows, int64_t
                     amax = fabsf(v);
             }
             float scale = amax > 0.0f ? amax / 448.0f : 1.0f;
+            if (scale == 0.0f)
+                scale = 1.0f; /* the quotient of a tiny f32 amax rounds to 0 */
             scales[r * groups + g] = scale;
             for (int64_t i = g * group; i < (g + 1) * group; ++i) {
                 float v = x_is_bf16 ? (float)oracle_bf16_to_double(((const uint16_t *)x)[r * h + i])
