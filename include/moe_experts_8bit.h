@@ -22,7 +22,7 @@
  * each other; a failed host check leaves every buffer untouched.
  *   - codes and bf16 buffers are 16-byte aligned, offsets 8-byte, scales 4-byte.
  *   - 1 <= num_experts <= MOE_MAX_EXPERTS; 0 <= max_rows < 2^31; max_rows * n <= 2^42.
- *   - Rows at and after off[num_experts] are not written, and what they hold has no effect.
+ *   - Rows at and after off[num_experts] are not read and not written.
  *   - Offsets that are not a valid prefix (off[0] != 0, a decreasing entry,
  *     the -1 of a rejected permute, off[num_experts] > max_rows) are detected
  *     on the device: then nothing is written.

@@ -9,6 +9,9 @@
 // a long one has a workgroup to itself (16384 rows of 7168 bf16 to int8: 58 us, 67
 // when walked).  Codes are stored non-temporally (200000 rows of 512: 57 us, 63
 // without; 8192 of 14336: 62, 71).  8192 rows of 14336 bf16, int8: 59.6 us, 5.9 TB/s.
+// With offsets the number of the experts' rows is read first and no other row is (16384
+// rows of 7168 bf16 to int8, 12.5 % / 30 % / all of them an expert's: 13 / 23 / 63 us, 40 / 45 /
+// 66 where rows were loaded ahead of it).
 
 #include <hip/hip_runtime.h>
 
@@ -25,6 +28,12 @@ namespace {
 constexpr int kHeldVecs = 4;   // vectors of a row per thread, 7 of 256 threads
 constexpr int64_t kMostWorkgroups = 1 << 20;  // times 1024 threads fit a launch
 constexpr int kMostThreads = 1024;
+// Workgroups of long rows per CU where offsets say which rows are an expert's: one
+// for each row of a large buffer with few such rows takes long to find out that it
+// has none (65536 rows of 7168 bf16 to fp8, 0.1 % / 12.5 % / all of them an expert's: 22 /
+// 50 / 258 us, with 64 per CU 7 / 35 / 241, with 32 5 / 35 / 248, with 8 5 / 37 / 285; 16384
+// of 4096 f32, all of them an expert's, 56 with 64, 61 with 32).
+constexpr int64_t kOffsetsPerCu = 64;
 
 struct QuantizeParams {
     const u32x4* x;
@@ -68,21 +77,22 @@ __global__ __launch_bounds__(kTpt > 256 ? kTpt : 256) void quantize_rows_kernel(
     const int t = (int)(threadIdx.x % kTpt);
     const int64_t stride = (int64_t)gridDim.x * kRows;
     int64_t row = (int64_t)blockIdx.x * kRows + __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kTpt));
+    int64_t rows = p.max_rows;
+    if (p.off != nullptr) {  // what lies behind the last expert's rows is not read
+        rows = wave_uniform64(p.off[p.num_experts]);
+        if (rows > p.max_rows || (int64_t)blockIdx.x * kRows >= rows) return;
+    }
     u32x4 next[kU];
     auto load = [&](int64_t r) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int idx = t + kTpt * u;
-            next[u] = r < p.max_rows && idx < p.rv ? __builtin_nontemporal_load(p.x + r * p.rv + idx)
-                                                   : u32x4{0u, 0u, 0u, 0u};
+            next[u] = r < rows && idx < p.rv ? __builtin_nontemporal_load(p.x + r * p.rv + idx)
+                                             : u32x4{0u, 0u, 0u, 0u};
         }
     };
     load(row);
-    int64_t rows = p.max_rows;
-    if (p.off != nullptr) {
-        if (!expert_offsets_valid<kThreads>(p.off, p.num_experts, p.max_rows)) return;
-        rows = wave_uniform64(p.off[p.num_experts]);
-    }
+    if (p.off != nullptr && !expert_offsets_valid<kThreads>(p.off, p.num_experts, p.max_rows)) return;
     for (; row < rows; row += stride) {
         u32x4 v[kU];
 #pragma unroll
@@ -126,7 +136,9 @@ template <typename Codes, bool kBF16, int kU, int kTpt>
 hipError_t launch_held(const QuantizeParams& p, int num_cus, hipStream_t stream) {
     constexpr int kThreads = kTpt > 256 ? kTpt : 256, kRows = kThreads / kTpt;
     const int64_t needed = (p.max_rows + kRows - 1) / kRows;
-    const int64_t most = kTpt == 64 ? (int64_t)num_cus * (2048 / kThreads) : kMostWorkgroups;
+    const int64_t most = kTpt == 64         ? (int64_t)num_cus * (2048 / kThreads)
+                         : p.off != nullptr ? (int64_t)num_cus * kOffsetsPerCu
+                                            : kMostWorkgroups;
     hipLaunchKernelGGL((quantize_rows_kernel<Codes, kBF16, kU, kTpt>), dim3((unsigned)(needed < most ? needed : most)),
                        dim3(kThreads), 0, stream, p);
     return hipGetLastError();
