@@ -31,7 +31,7 @@ SOURCES = ["moe_permute_wave.hip", "moe_permute_fused.hip", "moe_permute_coarse.
            "moe_quant_int8.hip", "moe_quantize_rows.hip", "moe_expert_8bit.hip", "moe_expert_stream8.hip",
            "moe_experts_8bit_api.cpp"]
 HEADERS = ["moe_launch.h", "moe_plan.h", "moe_permute_device.h", "moe_gemm_device.h", "moe_expert_launch.h",
-           "moe_expert_plan.h", "moe_expert_device.h", "moe_expert_tile.h", "moe_expert_tile_list.h",
+           "moe_expert_plan.h", "moe_expert_device.h", "moe_expert_tile.h", "moe_expert_tile_list.h", "moe_expert_tile_choice.h",
            "moe_quant_device.h", "moe_quant_kernel.h", "moe_expert_8bit_launch.h",
            "moe_expert_8bit_plan.h", "moe_api_checks.h"]
 PROBE_SOURCES = ["hbm_probe.hip"]  # streaming-ceiling kernels used by bench.py only

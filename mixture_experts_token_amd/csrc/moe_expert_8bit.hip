@@ -547,14 +547,8 @@ hipError_t launch_expert_8bit(const Expert8BitArgs& a, int num_cus, hipStream_t 
         const hipError_t err = launch_expert_stream8(a, plan, num_cus, stream);
         if (err != hipSuccess || a.rows.max_rows <= p.skip_rows) return err;  // no expert can have more
     }
-    const int64_t groups = most_groups(a.rows);
-    TileChoice tiles = choose_tiles(a.rows.max_rows, groups, a.n, a.gated ? 128 : 256, p.k, num_cus);
-    // With few rows per expert the work is streaming the weights, and small tiles
-    // leave fewer of a tile's rows empty.  Small / large, us: 100 rows per expert,
-    // 14336 x 4096 gated, 8 experts 219 / 243, 768 x 2048, 128 experts 104 / 109,
-    // 2048 x 768 71 / 78; 128 rows (half of the experts have more) 275 / 247,
-    // 132 / 111, 90 / 80.
-    if (streamed || a.rows.max_rows <= 112 * groups) tiles = {true, false};
+    const TileChoice tiles =
+        choose_tiles8(a.rows.max_rows, a.rows.num_experts, a.n, a.k, a.gated, streamed, num_cus);
     p.apart = tiles.apart;
     return a.int8 ? launch_tiles<Codes8::kInt8>(p, a, tiles.small, num_cus, stream)
                   : launch_tiles<Codes8::kFp8>(p, a, tiles.small, num_cus, stream);

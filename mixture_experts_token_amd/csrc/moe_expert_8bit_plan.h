@@ -1,10 +1,12 @@
 // moe_expert_8bit_plan.h -- which rows of the 8-bit layers are streamed
-// (moe_expert_stream8.hip) and which go to the tiles (moe_expert_8bit.hip).
+// (moe_expert_stream8.hip) and which go to the tiles (moe_expert_8bit.hip), and to which.
 // Pure C++, no HIP call: the rows of each expert are only known on the device, so
 // the plan bounds what any routing of max_rows rows can cost.
 #pragma once
 
 #include <cstdint>
+
+#include "moe_expert_tile_choice.h"
 
 namespace moe {
 
@@ -56,6 +58,18 @@ inline Stream8Plan plan_stream8(int64_t max_rows, int64_t num_experts, int64_t c
     }
     p.steps = stream8_steps(k, p.kw);
     return p;
+}
+
+// The tiles of what is not streamed.  With few rows per expert the work is streaming
+// the weights, and small tiles leave fewer of a tile's rows empty.  Small / large, us:
+// 100 rows per expert, 14336 x 4096 gated, 8 experts 219 / 243, 768 x 2048, 128
+// experts 104 / 109, 2048 x 768 71 / 78; 128 rows (half of the experts have more)
+// 275 / 247, 132 / 111, 90 / 80.
+inline TileChoice choose_tiles8(int64_t max_rows, int64_t num_experts, int64_t n, int64_t k, bool gated, bool streamed,
+                                int num_cus) {
+    const int64_t groups = max_rows < num_experts ? max_rows : num_experts;  // experts that may have rows
+    if (streamed || max_rows <= 112 * groups) return {true, false};
+    return choose_tiles(max_rows, groups, n, gated ? kLargeTile / 2 : kLargeTile, k / 2, num_cus);
 }
 
 }  // namespace moe

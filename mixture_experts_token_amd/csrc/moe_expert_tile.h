@@ -29,13 +29,13 @@
 #include <cstdint>
 
 #include "moe_expert_device.h"
+#include "moe_expert_tile_choice.h"
 
 namespace moe {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kStepT = 64;
 constexpr int kTileThreads = 512;
 constexpr int kHalfBytes = 128 * kStepT * 2;       // one half tile
 constexpr int kStageBytes = 4 * kHalfBytes;        // A0, A1, B0, B1
@@ -46,7 +46,7 @@ constexpr int kTileLds = 2 * kStageBytes;
 // four stages of one half tile of each operand.
 template <bool kSmall>
 struct TileShape {
-    static constexpr int kRows = kSmall ? 128 : 256, kCols = kSmall ? 128 : 256;
+    static constexpr int kRows = kSmall ? kSmallTile : kLargeTile, kCols = kRows;
     static constexpr int kHalves = kSmall ? 1 : 2;     // halves of 128 rows
     static constexpr int kBlocks = kSmall ? 1 : 2;     // 32-row blocks of a wave in a half
     static constexpr int kWavesAcross = kSmall ? 2 : 4;

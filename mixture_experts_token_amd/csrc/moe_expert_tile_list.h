@@ -1,6 +1,6 @@
 // moe_expert_tile_list.h -- what the expert layers' tiled products share beside the
-// tile itself (moe_expert_tile.h): the order of an expert's tiles, which of them
-// go to a launch of their own, the choice of tile, and results to memory.
+// tile itself (moe_expert_tile.h) and its choice (moe_expert_tile_choice.h): the
+// order of an expert's tiles and results to memory.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -10,16 +10,12 @@
 #include "moe_expert_device.h"
 #include "moe_expert_launch.h"
 #include "moe_expert_tile.h"
+#include "moe_expert_tile_choice.h"
 
 namespace moe {
 
 constexpr int kXcdCount = 8;
 constexpr int64_t kGroupRows = 8;  // row tiles per group in the tile order
-
-// Cost of a tile outside its k-loop, and of a small tile's step, in steps of a
-// large one (1.5 us with every CU busy; 10 us and 0.6 - 0.7 us measured).
-constexpr double kFixedCost = 6.0, kSmallStepCost = 0.45, kSmallFixedCost = 3.0;
-constexpr int64_t kApartMostRounds = 4;
 
 // Quotient and remainder of non-negative scalars; 32 bits when both fit (a
 // 64-bit division is a long sequence of instructions).
@@ -37,12 +33,6 @@ struct TileCoord {
     int64_t r0, c0;        // the tile's first output row (of the expert's) and column
 };
 
-// An expert's remainder of at most half a large tile's rows.
-__device__ __forceinline__ bool light_remainder(int64_t count) {
-    const int64_t left = count % TileShape<false>::kRows;
-    return left > 0 && left <= TileShape<true>::kRows;
-}
-
 // Which of an expert's rows a launch takes.
 enum class Part { kAll, kNoLight, kLight };
 
@@ -50,23 +40,6 @@ template <int kRows>
 __device__ __forceinline__ int64_t row_tiles(int64_t rows, Part part) {
     if (part == Part::kLight) return light_remainder(rows) ? 1 : 0;
     return (rows + kRows - 1) / kRows - (part == Part::kNoLight && light_remainder(rows) ? 1 : 0);
-}
-
-// Whether the tiles of the light remainders (light of them, beside heavy others)
-// are better taken as small tiles by a launch of their own: with few rounds of
-// workgroups, a last one of only some light tiles leaves most CUs idle for as
-// long as a whole tile takes (512 heavy and 64 light tiles of 224 steps, 256
-// CUs: 987 us in one launch, 891 in two).  Both launches ask this.  Costs in
-// hundredths of a step, as choose_tiles has them; past a few rounds the light
-// tiles fill gaps, and apart they would stream the weights again.
-__device__ __forceinline__ bool remainders_apart(int64_t heavy, int64_t light, int64_t depth, int64_t cus) {
-    if (light == 0 || heavy > kApartMostRounds * cus) return false;
-    const int64_t steps = (depth + kStepT - 1) / kStepT;
-    const int64_t large = steps * 100 + (int64_t)(kFixedCost * 100);
-    const int64_t small = (int64_t)(kSmallStepCost * 100) * steps + (int64_t)(kSmallFixedCost * 100);
-    const int64_t together = (heavy + light + cus - 1) / cus * large;
-    const int64_t split = (heavy + cus - 1) / cus * large + (2 * light + cus - 1) / cus * small;
-    return split < together / 10 * 9;
 }
 
 // Order of an expert's tiles: groups of kGroupRows row tiles, within a group
@@ -129,36 +102,6 @@ __device__ __forceinline__ void add4(f32x16& v, int j, u32x2 w) {
     v[4 * j + 1] += bf16_high(w[0]);
     v[4 * j + 2] += bf16_low(w[1]);
     v[4 * j + 3] += bf16_high(w[1]);
-}
-
-struct TileChoice {
-    bool small;   // 128 x 128 tiles
-    bool apart;   // large ones, with the light remainders perhaps in a launch of their own
-};
-
-// Whether a product runs faster on small tiles: its rounds of workgroups times
-// what a tile takes.  rows: output rows of all experts; groups: experts that may
-// have rows (each ends in half a tile on average).  Small / large tiles, us:
-// one expert 1024^3 18.1 / 27.9, 2048^3 29 / 54, 4096 x 4096 x 512 37.7 / 26.1;
-// 8 experts of 300 rows, 1024 x 1024 18 / 29.5, of 1024, 2048 x 2048 125 / 104;
-// 128 of 64, 768 x 2048 112 / 127, of 128 144 / 134.
-inline TileChoice choose_tiles(int64_t rows, int64_t groups, int64_t cols, int64_t cols_large, int64_t depth, int num_cus) {
-    const int64_t steps = (depth + kStepT - 1) / kStepT;
-    auto rounds = [&](int64_t tile, int64_t tile_cols) {
-        const int64_t row_tiles = (rows + tile - 1) / tile + (groups > 1 ? (groups - 1) / 2 : 0);
-        const int64_t tiles = row_tiles * ((cols + tile_cols - 1) / tile_cols);
-        return (tiles + num_cus - 1) / num_cus;
-    };
-    const int64_t large = rounds(256, cols_large);
-    TileChoice c;
-    c.small = (double)rounds(128, cols_large / 2) * ((double)steps * kSmallStepCost + kSmallFixedCost) <
-              (double)large * ((double)steps + kFixedCost);
-    // The second launch and its test cost some 7 us where it finds nothing to do;
-    // with fewer than three whole tiles per expert the light tiles' weights weigh
-    // more than the idle CUs (32 experts of 300 rows, 768 x 2048 gated: 92 us in
-    // one launch, 113 in two; 8 of 1024, 2048 x 2048: 99 / 92).
-    c.apart = !c.small && groups > 1 && rows >= 768 * groups && large <= kApartMostRounds + 1 && steps >= 16;
-    return c;
 }
 
 // One per CU; a multiple of the XCDs, among which the tile order divides them.
