@@ -16,8 +16,8 @@
 //     is read from LDS while loads into it are under way is read in inline asm
 //     (the compiler would wait for all of them).
 //
-// 8 experts of 1024 rows, 14336 x 4096 gated, int8: 886 - 929 us, 2.1 POP/s; 4096 x
-// 14336, fp8: 431 - 442 us, 2.2 PFLOP/s.  Power bounds them: MFMAs are busy 61 - 69 %
+// 8 experts of 1024 rows, 14336 x 4096 gated, int8: 867 - 950 us, 2.1 POP/s; 4096 x
+// 14336, fp8: 424 - 458 us, 2.2 PFLOP/s.  Power bounds them: MFMAs are busy 61 - 69 %
 // of the cycles of a clock at 1.4 - 1.9 GHz.
 
 #include <hip/hip_runtime.h>
